@@ -415,6 +415,120 @@ typedef struct {
 
 moe_status moe_ctx_timing(moe_ctx* ctx, moe_timing* out, int32_t reset);
 
+/* ------------------------------------------------------------------------
+ * Operators without a context: MXFP4 conversion and products, and the pieces
+ * of a routed FFN over weights that are resident in device memory (the pages'
+ * design keeps them in host memory; a layer that fits, a shared expert or a
+ * dense projection needs none of the slot machinery).  They follow the
+ * conventions above, and:
+ *   - every pointer is (device) and belongs to the device that is current;
+ *     `stream` is a stream of that device.  Nothing is kept between calls and
+ *     nothing is allocated, so any call may be captured into a HIP graph and
+ *     calls on different streams may overlap;
+ *   - outputs must not overlap inputs;
+ *   - an MXFP4 matrix is codes [rows][cols/2] and scales [rows][cols/32], both
+ *     contiguous, in the bank format (OCP MX v1.0 E2M1, low nibble = even
+ *     element, one E8M0 scale per 32 elements of a row; scale 255 is NaN);
+ *   - codes, scales' matrices and rows of x are addressed in 16-byte pieces:
+ *     base addresses of x and of codes are 16-byte aligned, and a leading
+ *     dimension (elements from one row to the next) keeps every row of x so.
+ *     y needs the alignment of its element only;
+ *   - a HIP failure is returned (MOE_EHIP) but not latched.
+ * A call with nothing to compute (no rows) returns MOE_OK. */
+
+/* Rows of x (F32 or BF16) to MXFP4.  Per block of 32: e = floor(log2 max|x|) -
+ * 2, at least -127 (a block of zeros: e = 0), scale byte e + 127, code = x *
+ * 2^-e rounded to nearest with ties to the even code, at most 6 in magnitude;
+ * a value that rounds to zero gets code 0 whatever its sign.  A block that
+ * holds an infinity or a NaN becomes NaN as a whole (scale 255, codes 0).
+ * x [rows][cols], ldx elements from row to row; cols % 32 == 0; ldx >= cols,
+ * a multiple of 16 bytes. */
+moe_status moe_mx_quantize(const void* x, moe_dtype x_dtype, int64_t rows, int32_t cols, int64_t ldx,
+                           uint8_t* codes, uint8_t* scales, moe_stream stream);
+
+/* The values that codes and scales stand for, as F32 or BF16 (exact, but for
+ * magnitudes past the largest finite value, which become infinite).
+ * y [rows][cols], ldy >= cols elements from row to row. */
+moe_status moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t cols,
+                             void* y, moe_dtype y_dtype, int64_t ldy, moe_stream stream);
+
+/* y[M][N] = x[M][K] * W[N][K]^T with W in MXFP4.  x is BF16 (x_scales NULL;
+ * ldx >= K elements from row to row) or MXFP4 (x holds codes, x_scales the
+ * scales; ldx must be K).  fp32 accumulation, one rounding to y_dtype (BF16 or
+ * F32).  K % 32 == 0, any N; ldy >= N.  MOE_EUNSUPPORTED for other dtypes. */
+moe_status moe_mx_gemm(const void* x, moe_dtype x_dtype, const uint8_t* x_scales, int64_t ldx,
+                       const uint8_t* w_codes, const uint8_t* w_scales, void* y, moe_dtype y_dtype,
+                       int64_t ldy, int32_t M, int32_t N, int32_t K, moe_stream stream);
+
+/* The T*k routed pairs (pair p = t*k + j) ordered by expert: offsets [E+1]
+ * receives the first position of each expert (offsets[E] = pairs with an
+ * expert in 0..E-1), perm [T*k] the pair at each position, pairs of one expert
+ * in ascending pair order; pairs whose id lies outside 0..E-1 (padding) take
+ * the positions from offsets[E] on, as -1.  1 <= E <= 1024, T*k < 2^31 - 4096.
+ * workspace (4-byte aligned) must hold moe_group_workspace(T, k, E) bytes (0
+ * for up to 4,096 pairs, then it may be NULL) and belongs to the call until its
+ * work has finished: calls that can overlap, captured graphs among them, need
+ * one each. */
+size_t moe_group_workspace(int32_t T, int32_t k, int32_t E);
+moe_status moe_group_pairs(const int32_t* ids, int32_t T, int32_t k, int32_t E, int32_t* offsets,
+                           int32_t* perm, void* workspace, size_t workspace_bytes, moe_stream stream);
+
+/* Ragged products grouped by expert.  Position p in [offsets[e], offsets[e+1])
+ * of the n_rows positions belongs to expert e:
+ *   row(p) = x[x_index ? x_index[p] / x_index_div : p] * W_e[N][K]^T
+ *   y[y_index ? y_index[p] : p] = row(p), or with glu = 1
+ *   silu(row(p)[0..N/2)) * row(p)[N/2..N)  (N/2 columns; gate rows first, then
+ *   up rows, as gate and up lie in a bank).
+ * Types (x, W): (BF16, BF16), (BF16, MXFP4), (MXFP4, MXFP4); y BF16 or F32;
+ * fp32 accumulation and SiLU, one rounding.  With x_index = perm, x_index_div
+ * = k the rows of x are tokens; with y_index = perm the rows of y are pairs.
+ * offsets and the indices are read on the device and never on the host:
+ * positions before offsets[0] or from offsets[E] on leave y as it was; an
+ * x_index outside 0..n_x-1 (after the division; negative ones too) reads a row
+ * of zeros; a y_index outside 0..n_y-1 writes nothing.  Offsets that do not
+ * ascend within 0..n_rows leave the affected rows unspecified but read and
+ * write nothing out of range.  If two positions name one row of y, which of
+ * the two it holds is unspecified.
+ * Expert e's weights are at w + e * w_stride bytes (rows contiguous; MXFP4
+ * scales at w_scales + e * ws_stride), so a matrix inside expert banks can be
+ * used in place.  w_stride is a multiple of 16 bytes and one expert's matrix
+ * stays below 2^31 bytes.  K % 32 == 0 where an operand is MXFP4, else K % 8
+ * == 0.  With x_index, the rows of x span less than 2^31 bytes. */
+typedef struct {
+  int32_t n_experts;         /* E (1..1024)                                       */
+  int32_t n_rows;            /* positions, >= 0                                   */
+  int32_t N, K;              /* rows of W_e; contraction                          */
+  int32_t x_dtype, w_dtype, y_dtype; /* moe_dtype                                 */
+  int32_t glu;               /* 0 or 1 (N even)                                   */
+  const void* x;             /* [n_x][K], ldx elements from row to row (MXFP4: K) */
+  const uint8_t* x_scales;   /* MXFP4 x: [n_x][K/32], else NULL                   */
+  int64_t ldx;
+  int32_t n_x;               /* rows of x; >= n_rows without x_index              */
+  int32_t x_index_div;       /* >= 1                                              */
+  const int32_t* x_index;    /* [n_rows] or NULL                                  */
+  const void* w;
+  const uint8_t* w_scales;   /* MXFP4 weights, else NULL                          */
+  int64_t w_stride, ws_stride; /* bytes from expert to expert                     */
+  const int32_t* offsets;    /* [E+1]                                             */
+  void* y;                   /* [n_y][N or N/2], ldy elements from row to row     */
+  int64_t ldy;
+  int32_t n_y;               /* rows of y; >= n_rows without y_index              */
+  int32_t reserved;          /* 0                                                 */
+  const int32_t* y_index;    /* [n_rows] or NULL                                  */
+} moe_grouped_args;
+
+moe_status moe_grouped_gemm(const moe_grouped_args* args, moe_stream stream);
+
+/* y[t] = sum over ascending j of w[t][j] * p[t*k + j] in fp32, one rounding:
+ * moe_merge's sum over rows that the caller holds.  p [T*k][H] (F32 or BF16,
+ * ldp elements from row to row), w fp32 [T][k], y [T][H] (F32 or BF16, ldy).
+ * ids [T][k] or NULL: pairs with an id outside 0..E-1 are left out (their rows
+ * are not read), so a token without any expert gives a row of zeros.
+ * Alignment: that of the elements. */
+moe_status moe_combine_pairs(const void* p, moe_dtype p_dtype, int64_t ldp, const float* w,
+                             const int32_t* ids, int32_t E, int32_t T, int32_t k, int32_t H, void* y,
+                             moe_dtype y_dtype, int64_t ldy, moe_stream stream);
+
 const char* moe_strerror(moe_status s);
 /* Text of the last error on the calling thread ("" if none). */
 const char* moe_last_error(void);

@@ -79,6 +79,18 @@ class Timing(ctypes.Structure):
         return {p: dict(calls=self.calls[i], ms=self.ms[i]) for i, p in enumerate(PHASES)}
 
 
+class GroupedArgs(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("glu", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("x_scales", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("n_x", ctypes.c_int32),
+                ("x_index_div", ctypes.c_int32), ("x_index", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("w_scales", ctypes.c_void_p), ("w_stride", ctypes.c_int64),
+                ("ws_stride", ctypes.c_int64), ("offsets", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("n_y", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("y_index", ctypes.c_void_p)]
+
+
 class MoertError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         self.status = status
@@ -122,6 +134,13 @@ def lib():
             "moe_prefill_view_get": ([vp, ctypes.POINTER(PrefillView)], i32),
             "moe_ctx_stats": ([vp, ctypes.POINTER(Stats)], i32),
             "moe_ctx_timing": ([vp, ctypes.POINTER(Timing), i32], i32),
+            "moe_mx_quantize": ([vp, i32, i64, i32, i64, vp, vp, vp], i32),
+            "moe_mx_dequantize": ([vp, vp, i64, i32, vp, i32, i64, vp], i32),
+            "moe_mx_gemm": ([vp, i32, vp, i64, vp, vp, vp, i32, i64, i32, i32, i32, vp], i32),
+            "moe_group_workspace": ([i32, i32, i32], sz),
+            "moe_group_pairs": ([vp, i32, i32, i32, vp, vp, vp, sz, vp], i32),
+            "moe_grouped_gemm": ([ctypes.POINTER(GroupedArgs), vp], i32),
+            "moe_combine_pairs": ([vp, i32, i64, vp, vp, i32, i32, i32, i32, vp, i32, i64, vp], i32),
             "moe_strerror": ([i32], ctypes.c_char_p),
             "moe_last_error": ([], ctypes.c_char_p),
         }
@@ -280,6 +299,175 @@ def moe_ctx_timing(ctx, reset=False) -> dict:
     t = Timing()
     _check(lib().moe_ctx_timing(ctx, ctypes.byref(t), 1 if reset else 0), "moe_ctx_timing")
     return t.as_dict()
+
+
+# ------------------------------------------------------------------ operators without a context
+# Sizes, dtypes and strides come from the tensors, so these also check what the
+# library cannot see: shapes that belong together, element types, contiguous
+# rows and one device.  The call is made with the tensors' device current, on
+# `stream` or on that device's current stream.
+_FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _need(ok, where, detail):
+    if not ok:
+        raise MoertError(MOE_EINVAL, where, detail)
+
+
+def _tensor(where, name, t, dims, dtypes, shape=None, contiguous=False):
+    """Checks one argument; `shape` entries of None are free."""
+    _need(isinstance(t, torch.Tensor), where, f"{name} must be a tensor")
+    _need(t.dim() == dims, where, f"{name} must have {dims} dimensions, has {t.dim()}")
+    _need(t.dtype in dtypes, where, f"{name}: dtype {t.dtype} is not one of {', '.join(map(str, dtypes))}")
+    if shape is not None:
+        _need(all(w is None or w == h for w, h in zip(shape, t.shape)), where,
+              f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if contiguous:
+        _need(t.is_contiguous(), where, f"{name} must be contiguous")
+    else:
+        _need(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1, where,
+              f"{name}: the elements of a row must be contiguous")
+    _need(max(t.shape, default=0) < 1 << 31, where, f"{name} is too large")
+
+
+def _ld(t):
+    """Elements from row to row of a matrix; a single row has no next one."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] + -t.shape[1] % 8
+
+
+def _call(where, fn, tensors, stream, *args):
+    """fn(*args, stream) with the tensors' common device current."""
+    tensors = [t for t in tensors if t is not None]
+    dev = tensors[0].device
+    _need(dev.type == "cuda", where, f"tensors must be on the GPU, not on {dev}")
+    _need(all(t.device == dev for t in tensors), where, "tensors are on different devices")
+    if isinstance(stream, torch.cuda.Stream):
+        _need(stream.device == dev, where, f"stream of {stream.device}, tensors on {dev}")
+    with torch.cuda.device(dev):
+        _check(fn(*args, _stream(stream)), where)
+
+
+def moe_mx_quantize(x, codes, scales, stream=None):
+    """x [R, C] f32 or bf16 (rows may be strided) -> codes uint8 [R, C/2], scales uint8 [R, C/32]."""
+    me = "moe_mx_quantize"
+    _tensor(me, "x", x, 2, tuple(_FLOATS))
+    R, C = x.shape
+    _need(C % 32 == 0, me, "the columns must be a multiple of 32")
+    _tensor(me, "codes", codes, 2, (torch.uint8,), (R, C // 2), True)
+    _tensor(me, "scales", scales, 2, (torch.uint8,), (R, C // 32), True)
+    _call(me, lib().moe_mx_quantize, (x, codes, scales), stream, _ptr(x), _FLOATS[x.dtype], R, C, _ld(x),
+          _ptr(codes), _ptr(scales))
+
+
+def moe_mx_dequantize(codes, scales, y, stream=None):
+    """codes uint8 [R, C/2], scales uint8 [R, C/32] -> y [R, C] f32 or bf16 (rows may be strided)."""
+    me = "moe_mx_dequantize"
+    _tensor(me, "y", y, 2, tuple(_FLOATS))
+    R, C = y.shape
+    _need(C % 32 == 0, me, "the columns must be a multiple of 32")
+    _tensor(me, "codes", codes, 2, (torch.uint8,), (R, C // 2), True)
+    _tensor(me, "scales", scales, 2, (torch.uint8,), (R, C // 32), True)
+    _call(me, lib().moe_mx_dequantize, (y, codes, scales), stream, _ptr(codes), _ptr(scales), R, C, _ptr(y),
+          _FLOATS[y.dtype], _ld(y))
+
+
+def _rows_operand(me, x, x_scales):
+    """(K, dtype, ldx) of x: bf16 rows, or codes with their scales."""
+    if x_scales is None:
+        _tensor(me, "x", x, 2, (torch.bfloat16,))
+        return x.shape[1], MOE_BF16, _ld(x)
+    _tensor(me, "x", x, 2, (torch.uint8,), contiguous=True)
+    K = x.shape[1] * 2
+    _need(K % 32 == 0, me, "K must be a multiple of 32")
+    _tensor(me, "x_scales", x_scales, 2, (torch.uint8,), (x.shape[0], K // 32), True)
+    return K, MOE_MXFP4, K
+
+
+def moe_mx_gemm(x, w_codes, w_scales, y, x_scales=None, stream=None):
+    """y [M, N] (f32 or bf16) = x W^T, W as codes uint8 [N, K/2] and scales uint8
+    [N, K/32]; x bf16 [M, K], or codes uint8 [M, K/2] with x_scales [M, K/32]."""
+    me = "moe_mx_gemm"
+    K, x_dtype, ldx = _rows_operand(me, x, x_scales)
+    _need(K % 32 == 0, me, "K must be a multiple of 32")
+    _tensor(me, "w_codes", w_codes, 2, (torch.uint8,), (None, K // 2), True)
+    N = w_codes.shape[0]
+    _tensor(me, "w_scales", w_scales, 2, (torch.uint8,), (N, K // 32), True)
+    _tensor(me, "y", y, 2, tuple(_FLOATS), (x.shape[0], N))
+    _call(me, lib().moe_mx_gemm, (x, x_scales, w_codes, w_scales, y), stream, _ptr(x), x_dtype,
+          _ptr(x_scales), ldx, _ptr(w_codes), _ptr(w_scales), _ptr(y), _FLOATS[y.dtype], _ld(y), x.shape[0],
+          N, K)
+
+
+def moe_group_workspace(T, k, E):
+    return lib().moe_group_workspace(T, k, E)
+
+
+def moe_group_pairs(ids, n_experts, offsets, perm, workspace=None, stream=None):
+    """ids int32 [T, k] -> offsets int32 [E+1], perm int32 [T*k]; workspace: any
+    contiguous tensor of at least moe_group_workspace(T, k, E) bytes."""
+    me = "moe_group_pairs"
+    i32 = (torch.int32,)
+    _tensor(me, "ids", ids, 2, i32, contiguous=True)
+    T, k = ids.shape
+    _tensor(me, "offsets", offsets, 1, i32, (n_experts + 1,), True)
+    _tensor(me, "perm", perm, 1, i32, (T * k,), True)
+    nbytes = 0
+    if workspace is not None:
+        _need(workspace.is_contiguous(), me, "workspace must be contiguous")
+        nbytes = workspace.numel() * workspace.element_size()
+    _call(me, lib().moe_group_pairs, (ids, offsets, perm, workspace), stream, _ptr(ids), T, k, n_experts,
+          _ptr(offsets), _ptr(perm), _ptr(workspace), nbytes)
+
+
+def moe_grouped_gemm(x, w, offsets, y, x_scales=None, w_scales=None, x_index=None, x_index_div=1,
+                     y_index=None, glu=False, stream=None):
+    """Row p of the positions offsets[e] <= p < offsets[e+1] times expert e's W^T.
+    x bf16 [n_x, K] or codes [n_x, K/2] with x_scales; w bf16 [E, N, K] or codes
+    [E, N, K/2] with w_scales [E, N, K/32] (any stride from expert to expert);
+    y [n_y, N], or [n_y, N/2] with glu; x_index, y_index int32 [n_rows].  The
+    positions are those of an index, else the rows of x."""
+    me = "moe_grouped_gemm"
+    K, x_dtype, ldx = _rows_operand(me, x, x_scales)
+    i32 = (torch.int32,)
+    if w_scales is None:
+        _tensor(me, "w", w, 3, (torch.bfloat16,), (None, None, K))
+        w_dtype, row = MOE_BF16, K
+    else:
+        _tensor(me, "w", w, 3, (torch.uint8,), (None, None, K // 2))
+        _tensor(me, "w_scales", w_scales, 3, (torch.uint8,), (w.shape[0], w.shape[1], K // 32))
+        _need(w.shape[1] == 1 or w_scales.stride(1) == K // 32, me, "w_scales: rows of one expert must be contiguous")
+        w_dtype, row = MOE_MXFP4, K // 2
+    E, N = w.shape[:2]
+    _need(N == 1 or w.stride(1) == row, me, "w: rows of one expert must be contiguous")
+    _tensor(me, "offsets", offsets, 1, i32, (E + 1,), True)
+    index = x_index if x_index is not None else y_index
+    n_rows = x.shape[0] if index is None else index.shape[0]
+    for name, t in (("x_index", x_index), ("y_index", y_index)):
+        if t is not None:
+            _tensor(me, name, t, 1, i32, (n_rows,), True)
+    _tensor(me, "y", y, 2, tuple(_FLOATS), (None, N // 2 if glu else N))
+    size = w.element_size()
+    a = GroupedArgs(E, n_rows, N, K, x_dtype, w_dtype, _FLOATS[y.dtype], 1 if glu else 0, _ptr(x),
+                    _ptr(x_scales), ldx, x.shape[0], x_index_div, _ptr(x_index), _ptr(w), _ptr(w_scales),
+                    w.stride(0) * size if E > 1 else 0, w_scales.stride(0) if w_scales is not None and E > 1 else 0,
+                    _ptr(offsets), _ptr(y), _ld(y), y.shape[0], 0, _ptr(y_index))
+    _call(me, lib().moe_grouped_gemm, (x, x_scales, w, w_scales, offsets, y, x_index, y_index), stream,
+          ctypes.byref(a))
+
+
+def moe_combine_pairs(p, w, y, ids=None, n_experts=0, stream=None):
+    """y [T, H] = sum over j of w[t, j] * p[t*k + j]; p [T*k, H], w f32 [T, k];
+    with ids int32 [T, k], pairs outside 0..n_experts-1 are left out."""
+    me = "moe_combine_pairs"
+    _tensor(me, "w", w, 2, (torch.float32,), contiguous=True)
+    T, k = w.shape
+    _tensor(me, "p", p, 2, tuple(_FLOATS), (T * k, None))
+    H = p.shape[1]
+    _tensor(me, "y", y, 2, tuple(_FLOATS), (T, H))
+    if ids is not None:
+        _tensor(me, "ids", ids, 2, (torch.int32,), (T, k), True)
+    _call(me, lib().moe_combine_pairs, (p, w, y, ids), stream, _ptr(p), _FLOATS[p.dtype], _ld(p), _ptr(w),
+          _ptr(ids), n_experts, T, k, H, _ptr(y), _FLOATS[y.dtype], _ld(y))
 
 
 def moe_strerror(status: int) -> str:

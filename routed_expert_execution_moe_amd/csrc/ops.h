@@ -1,0 +1,157 @@
+// Shared by the operators that need no context: launcher declarations, the
+// device-side arguments of the (grouped) products and their common device
+// code.
+#pragma once
+
+#include <algorithm>
+#include <tuple>
+
+#include "internal.h"
+
+namespace moert {
+
+// ------------------------------------------------------------------ launchers
+// hipLaunchKernel's own status: an error that an earlier caller left behind in
+// the thread is neither taken for this launch's nor cleared
+template <typename... P, typename... A>
+inline hipError_t launch_op(void (*f)(P...), dim3 grid, dim3 block, hipStream_t s, A... a) {
+  std::tuple<P...> p(a...);
+  return std::apply(
+      [&](auto&... v) {
+        void* ptrs[] = {(void*)&v...};
+        return hipLaunchKernel((const void*)f, grid, block, ptrs, 0, s);
+      },
+      p);
+}
+
+// Operands of y = x W^T, grouped by expert; a dense product is one group
+// (offsets == nullptr) of n_rows rows.
+struct ProductArgs {
+  const uint8_t* x;         // rows of bf16 or of MXFP4 codes
+  const uint8_t* xs;        // [n_x][K/32] scales of MXFP4 rows
+  const uint8_t* w;         // expert e at w + e * w_stride, [N][K]
+  const uint8_t* ws;        // [N][K/32] at ws + e * ws_stride
+  int64_t x_ld;             // bytes from row to row of x
+  int64_t w_stride, ws_stride;
+  const int32_t* x_index;   // [n_rows] or nullptr
+  const int32_t* y_index;   // [n_rows] or nullptr
+  const int32_t* offsets;   // [E+1] or nullptr
+  void* y;
+  int64_t ldy;              // elements
+  int n_experts, n_rows, n_x, n_y, x_div, N, K, y_f32;
+};
+
+hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int cols, int64_t ldx, uint8_t* codes,
+                              uint8_t* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
+                                void* y, bool f32, int64_t ldy, hipStream_t s);
+// x_dtype / w_dtype as in moe_grouped_gemm; hipErrorInvalidConfiguration when
+// the product needs more workgroups than a launch may have
+hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool glu, hipStream_t s);
+size_t group_workspace(int64_t pairs, int E);
+hipError_t launch_group_pairs(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* perm,
+                              int32_t* ws, hipStream_t s);
+hipError_t launch_combine_pairs(const void* p, bool p_f32, int64_t ldp, const float* w, const int32_t* ids,
+                                int E, int T, int k, int H, void* y, bool y_f32, int64_t ldy, hipStream_t s);
+
+// ------------------------------------------------------------------ device code
+#if defined(__HIPCC__)
+typedef __bf16 op_bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 op_bf16x8 __attribute__((ext_vector_type(8)));
+typedef float op_f32x2 __attribute__((ext_vector_type(2)));
+typedef float op_f32x4 __attribute__((ext_vector_type(4)));
+typedef float op_f32x16 __attribute__((ext_vector_type(16)));
+typedef int op_i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned int op_u32x4 __attribute__((ext_vector_type(4)));
+
+// E8M0 byte to the float whose exponent the scaled converts use: byte 0 is
+// 2^-127 (a subnormal), byte 255 an infinity, which the converts turn into NaN
+__device__ inline float op_scale(uint32_t s) { return __uint_as_float(s ? s << 23 : 0x00400000u); }
+
+// round to nearest even, NaN stays NaN
+__device__ inline uint16_t op_bf16(float v) {
+  const __bf16 b = (__bf16)v;
+  return __builtin_bit_cast(uint16_t, b);
+}
+
+// 8 MXFP4 codes times their block's scale to bf16 (exact)
+__device__ inline op_bf16x8 op_fp4x8(uint32_t raw, float scale) {
+  const op_bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, scale, 0);
+  const op_bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, scale, 1);
+  const op_bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, scale, 2);
+  const op_bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(raw, scale, 3);
+  return op_bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// silu(g) * u.  exp(-g) overflows to infinity for g < -88 and the quotient
+// becomes a zero: the limit, for finite u.
+__device__ inline float op_silu_mul(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+
+struct OpTile {
+  int e, pos0, rows;  // expert, first position, positions (1..BM)
+};
+
+// The t-th BM-row tile over all groups, by one wave on its own (every lane
+// gets the answer): lane l sums the tiles of its E/64 experts, a wave scan
+// finds the lane, a walk over its experts the expert.  Offsets are clamped
+// into 0..n_rows, so bad ones cost results but no access out of range.
+__device__ inline bool op_find_tile(const ProductArgs& a, int BM, int t, OpTile* out) {
+  if (!a.offsets) {
+    out->e = 0;
+    out->pos0 = t * BM;
+    out->rows = min(BM, a.n_rows - out->pos0);
+    return out->rows > 0;
+  }
+  const int lane = threadIdx.x & 63, per = (a.n_experts + 63) >> 6;
+  auto range = [&](int e, int* lo) {
+    *lo = min(max(a.offsets[e], 0), a.n_rows);
+    return max(min(max(a.offsets[e + 1], 0), a.n_rows) - *lo, 0);
+  };
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    int lo;
+    if (e < a.n_experts) mine += (range(e, &lo) + BM - 1) / BM;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  const uint64_t past = __ballot(incl > t);
+  if (!past) return false;
+  const int owner = __builtin_ctzll(past);
+  int left = t - __builtin_amdgcn_readlane(incl - mine, owner);
+  for (int e = owner * per; e < a.n_experts; ++e) {
+    int lo;
+    const int n = range(e, &lo), tiles = (n + BM - 1) / BM;
+    if (left < tiles) {
+      out->e = e;
+      out->pos0 = lo + left * BM;
+      out->rows = min(BM, n - left * BM);
+      return true;
+    }
+    left -= tiles;
+  }
+  return false;
+}
+
+// Row of x that position p reads, -1 for a row of zeros.
+__device__ inline int op_x_row(const ProductArgs& a, int p) {
+  if (!a.x_index) return p;
+  const int i = a.x_index[p];
+  if (i < 0) return -1;
+  const int r = a.x_div == 1 ? i : i / a.x_div;
+  return r < a.n_x ? r : -1;
+}
+
+// Row of y that position p writes, -1 for none.
+__device__ inline int op_y_row(const ProductArgs& a, int p) {
+  if (!a.y_index) return p;
+  const int i = a.y_index[p];
+  return i < a.n_y ? i : -1;
+}
+#endif
+
+}  // namespace moert
