@@ -20,7 +20,8 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 
 HIP_SOURCES = ["route.hip", "plan.hip", "decode.hip", "ffn_f32.hip", "ffn_bf16.hip", "ffn_mx.hip",
-               "prefill.hip", "mx.hip", "pairs.hip", "product.hip", "ctx.cpp", "ops.cpp"]
+               "prefill.hip", "mx.hip", "pairs.hip", "product.hip", "product_tile_bf16.hip",
+               "product_tile_w4.hip", "product_tile_mx.hip", "ctx.cpp", "ops.cpp"]
 HOST_SOURCES = ["cpu_branch.cpp"]
 HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-Wall",
              "-Wno-unused-function", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

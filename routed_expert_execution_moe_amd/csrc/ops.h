@@ -48,6 +48,10 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 // x_dtype / w_dtype as in moe_grouped_gemm; hipErrorInvalidConfiguration when
 // the product needs more workgroups than a launch may have
 hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool glu, hipStream_t s);
+// its variant for many rows (product_tile.h), one source file per pair of types
+hipError_t launch_tile_bf16(const ProductArgs& a, bool glu, hipStream_t s);
+hipError_t launch_tile_w4(const ProductArgs& a, bool glu, hipStream_t s);
+hipError_t launch_tile_mx(const ProductArgs& a, bool glu, hipStream_t s);
 size_t group_workspace(int64_t pairs, int E);
 hipError_t launch_group_pairs(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* perm,
                               int32_t* ws, hipStream_t s);
@@ -91,53 +95,71 @@ struct OpTile {
   int e, pos0, rows;  // expert, first position, positions (1..BM)
 };
 
-// The t-th BM-row tile over all groups, by one wave on its own (every lane
-// gets the answer): lane l sums the tiles of its E/64 experts, a wave scan
-// finds the lane, a walk over its experts the expert.  Offsets are clamped
-// into 0..n_rows, so bad ones cost results but no access out of range.
-__device__ inline bool op_find_tile(const ProductArgs& a, int BM, int t, OpTile* out) {
-  if (!a.offsets) {
-    out->e = 0;
-    out->pos0 = t * BM;
-    out->rows = min(BM, a.n_rows - out->pos0);
-    return out->rows > 0;
-  }
-  const int lane = threadIdx.x & 63, per = (a.n_experts + 63) >> 6;
-  auto range = [&](int e, int* lo) {
+// The BM-row tiles of all groups, expert by expert.  One wave on its own: lane
+// l counts the tiles of its E/64 experts and a wave scan orders them; every
+// lane then gets the total, and find() the t-th tile.  Offsets are clamped into
+// 0..n_rows, so bad ones cost results but no access out of range.
+struct OpTiles {
+  int incl, mine, total;
+
+  static __device__ inline int range(const ProductArgs& a, int e, int* lo) {
     *lo = min(max(a.offsets[e], 0), a.n_rows);
     return max(min(max(a.offsets[e + 1], 0), a.n_rows) - *lo, 0);
-  };
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    int lo;
-    if (e < a.n_experts) mine += (range(e, &lo) + BM - 1) / BM;
   }
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d);
-    if (lane >= d) incl += v;
-  }
-  const uint64_t past = __ballot(incl > t);
-  if (!past) return false;
-  const int owner = __builtin_ctzll(past);
-  int left = t - __builtin_amdgcn_readlane(incl - mine, owner);
-  for (int e = owner * per; e < a.n_experts; ++e) {
-    int lo;
-    const int n = range(e, &lo), tiles = (n + BM - 1) / BM;
-    if (left < tiles) {
-      out->e = e;
-      out->pos0 = lo + left * BM;
-      out->rows = min(BM, n - left * BM);
-      return true;
+
+  __device__ inline OpTiles(const ProductArgs& a, int BM) : incl(0), mine(0) {
+    if (!a.offsets) {
+      total = (a.n_rows + BM - 1) / BM;
+      return;
     }
-    left -= tiles;
+    const int lane = threadIdx.x & 63, per = (a.n_experts + 63) >> 6;
+    for (int i = 0; i < per; ++i) {
+      const int e = lane * per + i;
+      int lo;
+      if (e < a.n_experts) mine += (range(a, e, &lo) + BM - 1) / BM;
+    }
+    incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d);
+      if (lane >= d) incl += v;
+    }
+    total = __builtin_amdgcn_readlane(incl, 63);
   }
-  return false;
+
+  __device__ inline bool find(const ProductArgs& a, int BM, int t, OpTile* out) const {
+    if (!a.offsets) {
+      out->e = 0;
+      out->pos0 = t * BM;
+      out->rows = min(BM, a.n_rows - out->pos0);
+      return t < total;
+    }
+    const uint64_t past = __ballot(incl > t);
+    if (!past) return false;
+    const int owner = __builtin_ctzll(past), per = (a.n_experts + 63) >> 6;
+    int left = t - __builtin_amdgcn_readlane(incl - mine, owner);
+    for (int e = owner * per; e < a.n_experts; ++e) {
+      int lo;
+      const int n = range(a, e, &lo), tiles = (n + BM - 1) / BM;
+      if (left < tiles) {
+        out->e = e;
+        out->pos0 = lo + left * BM;
+        out->rows = min(BM, n - left * BM);
+        return true;
+      }
+      left -= tiles;
+    }
+    return false;
+  }
+};
+
+// tiles of bm rows that n_rows positions in E groups can make at most
+inline int64_t op_max_tiles(const ProductArgs& a, int bm) {
+  if (!a.offsets) return (a.n_rows + bm - 1) / bm;
+  return a.n_rows / bm + std::min(a.n_experts, a.n_rows);
 }
 
-// Row of x that position p reads, -1 for a row of zeros.
+// Row of x that position p reads, -1 for none (the product is a row of zeros).
 __device__ inline int op_x_row(const ProductArgs& a, int p) {
   if (!a.x_index) return p;
   const int i = a.x_index[p];

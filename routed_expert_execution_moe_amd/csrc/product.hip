@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kSmWaves * 64) void product_small_kernel(ProductArg
   const int n_blocks = (n_out + 15) >> 4;
   const int nb = blockIdx.x % n_blocks;
   OpTile t;
-  if (!op_find_tile(a, MI * 16, blockIdx.x / n_blocks, &t)) return;
+  if (!OpTiles(a, MI * 16).find(a, MI * 16, blockIdx.x / n_blocks, &t)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -152,7 +152,8 @@ __global__ __launch_bounds__(kSmWaves * 64) void product_small_kernel(ProductArg
     for (int q = 0; q < 4; ++q) {
       const int n = nb * 16 + 4 * g + q;
       if (n >= n_out) continue;
-      const float v = GLU ? op_silu_mul(acc[i][0][q], acc[i][NB - 1][q]) : acc[i][0][q];
+      const float z = GLU ? op_silu_mul(acc[i][0][q], acc[i][NB - 1][q]) : acc[i][0][q];
+      const float v = live[i] ? z : 0.f;
       const int64_t at = (int64_t)row * a.ldy + n;
       if (a.y_f32) ((float*)a.y)[at] = v;
       else ((uint16_t*)a.y)[at] = op_bf16(v);
@@ -160,17 +161,11 @@ __global__ __launch_bounds__(kSmWaves * 64) void product_small_kernel(ProductArg
   }
 }
 
-// tiles of bm rows that n_rows positions in E groups can make
-static int64_t max_tiles(const ProductArgs& a, int bm) {
-  if (!a.offsets) return (a.n_rows + bm - 1) / bm;
-  return a.n_rows / bm + std::min(a.n_experts, a.n_rows);
-}
-
 template <int AT, int WT, bool GLU>
 static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
   const int64_t n_blocks = ((GLU ? a.N / 2 : a.N) + 15) / 16;
   const bool few = a.n_rows <= 16 * (int64_t)a.n_experts;
-  const int64_t wgs = max_tiles(a, few ? 16 : 64) * n_blocks;
+  const int64_t wgs = op_max_tiles(a, few ? 16 : 64) * n_blocks;
   if (wgs * kSmWaves * 64 >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   return launch_op(few ? product_small_kernel<AT, WT, GLU, 1> : product_small_kernel<AT, WT, GLU, 4>,
                    dim3((unsigned)wgs), dim3(kSmWaves * 64), s, a);
@@ -178,6 +173,14 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
 
 template <int AT, int WT>
 static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
+  // The tile kernel addresses the rows of x of a tile with 32-bit offsets and
+  // reads MXFP4 scales 8 at a time.
+  const bool tile_ok = a.x_ld < (1 << 23) && (AT != MOE_MXFP4 || a.K >= 256);
+  if (a.n_rows > 16 * (int64_t)a.n_experts && tile_ok) {
+    if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, s);
+    else if constexpr (WT == MOE_MXFP4) return launch_tile_w4(a, glu, s);
+    else return launch_tile_bf16(a, glu, s);
+  }
   return glu ? launch_small<AT, WT, true>(a, s) : launch_small<AT, WT, false>(a, s);
 }
 
