@@ -307,6 +307,7 @@ def moe_ctx_timing(ctx, reset=False) -> dict:
 # rows and one device.  The call is made with the tensors' device current, on
 # `stream` or on that device's current stream.
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_U8, _I32, _BF16, _F32 = (torch.uint8,), (torch.int32,), (torch.bfloat16,), (torch.float32,)
 
 
 def _need(ok, where, detail):
@@ -315,7 +316,13 @@ def _need(ok, where, detail):
 
 
 def _tensor(where, name, t, dims, dtypes, shape=None, contiguous=False):
-    """Checks one argument; `shape` entries of None are free."""
+    """Checks one argument; `shape` entries of None are free.  A whole contiguous
+    tensor of the expected shape, the usual case, takes one line: these checks
+    are host time in front of kernels of a few microseconds."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous() and t.numel() < 1 << 31:
+        have = t.shape
+        if len(have) == dims and (shape is None or have == shape or shape[0] is None and have[-1] == shape[-1]):
+            return  # every shape given with free entries fixes the last one only
     _need(isinstance(t, torch.Tensor), where, f"{name} must be a tensor")
     _need(t.dim() == dims, where, f"{name} must have {dims} dimensions, has {t.dim()}")
     _need(t.dtype in dtypes, where, f"{name}: dtype {t.dtype} is not one of {', '.join(map(str, dtypes))}")
@@ -337,24 +344,32 @@ def _ld(t):
 
 def _call(where, fn, tensors, stream, *args):
     """fn(*args, stream) with the tensors' common device current."""
-    tensors = [t for t in tensors if t is not None]
-    dev = tensors[0].device
-    _need(dev.type == "cuda", where, f"tensors must be on the GPU, not on {dev}")
-    _need(all(t.device == dev for t in tensors), where, "tensors are on different devices")
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            _need(t.is_cuda, where, f"tensors must be on the GPU, not on {t.device}")
+            _need(False, where, "tensors are on different devices")
     if isinstance(stream, torch.cuda.Stream):
-        _need(stream.device == dev, where, f"stream of {stream.device}, tensors on {dev}")
-    with torch.cuda.device(dev):
-        _check(fn(*args, _stream(stream)), where)
+        _need(stream.device.index == dev, where, f"stream of {stream.device}, tensors on cuda:{dev}")
+    if dev == torch._C._cuda_getDevice():
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(dev)
+        status = fn(*args, stream if isinstance(stream, int) else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(stream))
+    if status != MOE_OK:
+        _check(status, where)
 
 
 def moe_mx_quantize(x, codes, scales, stream=None):
     """x [R, C] f32 or bf16 (rows may be strided) -> codes uint8 [R, C/2], scales uint8 [R, C/32]."""
     me = "moe_mx_quantize"
-    _tensor(me, "x", x, 2, tuple(_FLOATS))
+    _tensor(me, "x", x, 2, _FLOATS)
     R, C = x.shape
     _need(C % 32 == 0, me, "the columns must be a multiple of 32")
-    _tensor(me, "codes", codes, 2, (torch.uint8,), (R, C // 2), True)
-    _tensor(me, "scales", scales, 2, (torch.uint8,), (R, C // 32), True)
+    _tensor(me, "codes", codes, 2, _U8, (R, C // 2), True)
+    _tensor(me, "scales", scales, 2, _U8, (R, C // 32), True)
     _call(me, lib().moe_mx_quantize, (x, codes, scales), stream, _ptr(x), _FLOATS[x.dtype], R, C, _ld(x),
           _ptr(codes), _ptr(scales))
 
@@ -362,11 +377,11 @@ def moe_mx_quantize(x, codes, scales, stream=None):
 def moe_mx_dequantize(codes, scales, y, stream=None):
     """codes uint8 [R, C/2], scales uint8 [R, C/32] -> y [R, C] f32 or bf16 (rows may be strided)."""
     me = "moe_mx_dequantize"
-    _tensor(me, "y", y, 2, tuple(_FLOATS))
+    _tensor(me, "y", y, 2, _FLOATS)
     R, C = y.shape
     _need(C % 32 == 0, me, "the columns must be a multiple of 32")
-    _tensor(me, "codes", codes, 2, (torch.uint8,), (R, C // 2), True)
-    _tensor(me, "scales", scales, 2, (torch.uint8,), (R, C // 32), True)
+    _tensor(me, "codes", codes, 2, _U8, (R, C // 2), True)
+    _tensor(me, "scales", scales, 2, _U8, (R, C // 32), True)
     _call(me, lib().moe_mx_dequantize, (y, codes, scales), stream, _ptr(codes), _ptr(scales), R, C, _ptr(y),
           _FLOATS[y.dtype], _ld(y))
 
@@ -374,12 +389,12 @@ def moe_mx_dequantize(codes, scales, y, stream=None):
 def _rows_operand(me, x, x_scales):
     """(K, dtype, ldx) of x: bf16 rows, or codes with their scales."""
     if x_scales is None:
-        _tensor(me, "x", x, 2, (torch.bfloat16,))
+        _tensor(me, "x", x, 2, _BF16)
         return x.shape[1], MOE_BF16, _ld(x)
-    _tensor(me, "x", x, 2, (torch.uint8,), contiguous=True)
+    _tensor(me, "x", x, 2, _U8, contiguous=True)
     K = x.shape[1] * 2
     _need(K % 32 == 0, me, "K must be a multiple of 32")
-    _tensor(me, "x_scales", x_scales, 2, (torch.uint8,), (x.shape[0], K // 32), True)
+    _tensor(me, "x_scales", x_scales, 2, _U8, (x.shape[0], K // 32), True)
     return K, MOE_MXFP4, K
 
 
@@ -389,10 +404,10 @@ def moe_mx_gemm(x, w_codes, w_scales, y, x_scales=None, stream=None):
     me = "moe_mx_gemm"
     K, x_dtype, ldx = _rows_operand(me, x, x_scales)
     _need(K % 32 == 0, me, "K must be a multiple of 32")
-    _tensor(me, "w_codes", w_codes, 2, (torch.uint8,), (None, K // 2), True)
+    _tensor(me, "w_codes", w_codes, 2, _U8, (None, K // 2), True)
     N = w_codes.shape[0]
-    _tensor(me, "w_scales", w_scales, 2, (torch.uint8,), (N, K // 32), True)
-    _tensor(me, "y", y, 2, tuple(_FLOATS), (x.shape[0], N))
+    _tensor(me, "w_scales", w_scales, 2, _U8, (N, K // 32), True)
+    _tensor(me, "y", y, 2, _FLOATS, (x.shape[0], N))
     _call(me, lib().moe_mx_gemm, (x, x_scales, w_codes, w_scales, y), stream, _ptr(x), x_dtype,
           _ptr(x_scales), ldx, _ptr(w_codes), _ptr(w_scales), _ptr(y), _FLOATS[y.dtype], _ld(y), x.shape[0],
           N, K)
@@ -406,11 +421,10 @@ def moe_group_pairs(ids, n_experts, offsets, perm, workspace=None, stream=None):
     """ids int32 [T, k] -> offsets int32 [E+1], perm int32 [T*k]; workspace: any
     contiguous tensor of at least moe_group_workspace(T, k, E) bytes."""
     me = "moe_group_pairs"
-    i32 = (torch.int32,)
-    _tensor(me, "ids", ids, 2, i32, contiguous=True)
+    _tensor(me, "ids", ids, 2, _I32, contiguous=True)
     T, k = ids.shape
-    _tensor(me, "offsets", offsets, 1, i32, (n_experts + 1,), True)
-    _tensor(me, "perm", perm, 1, i32, (T * k,), True)
+    _tensor(me, "offsets", offsets, 1, _I32, (n_experts + 1,), True)
+    _tensor(me, "perm", perm, 1, _I32, (T * k,), True)
     nbytes = 0
     if workspace is not None:
         _need(workspace.is_contiguous(), me, "workspace must be contiguous")
@@ -428,24 +442,23 @@ def moe_grouped_gemm(x, w, offsets, y, x_scales=None, w_scales=None, x_index=Non
     positions are those of an index, else the rows of x."""
     me = "moe_grouped_gemm"
     K, x_dtype, ldx = _rows_operand(me, x, x_scales)
-    i32 = (torch.int32,)
     if w_scales is None:
-        _tensor(me, "w", w, 3, (torch.bfloat16,), (None, None, K))
+        _tensor(me, "w", w, 3, _BF16, (None, None, K))
         w_dtype, row = MOE_BF16, K
     else:
-        _tensor(me, "w", w, 3, (torch.uint8,), (None, None, K // 2))
-        _tensor(me, "w_scales", w_scales, 3, (torch.uint8,), (w.shape[0], w.shape[1], K // 32))
+        _tensor(me, "w", w, 3, _U8, (None, None, K // 2))
+        _tensor(me, "w_scales", w_scales, 3, _U8, (w.shape[0], w.shape[1], K // 32))
         _need(w.shape[1] == 1 or w_scales.stride(1) == K // 32, me, "w_scales: rows of one expert must be contiguous")
         w_dtype, row = MOE_MXFP4, K // 2
     E, N = w.shape[:2]
     _need(N == 1 or w.stride(1) == row, me, "w: rows of one expert must be contiguous")
-    _tensor(me, "offsets", offsets, 1, i32, (E + 1,), True)
+    _tensor(me, "offsets", offsets, 1, _I32, (E + 1,), True)
     index = x_index if x_index is not None else y_index
     n_rows = x.shape[0] if index is None else index.shape[0]
     for name, t in (("x_index", x_index), ("y_index", y_index)):
         if t is not None:
-            _tensor(me, name, t, 1, i32, (n_rows,), True)
-    _tensor(me, "y", y, 2, tuple(_FLOATS), (None, N // 2 if glu else N))
+            _tensor(me, name, t, 1, _I32, (n_rows,), True)
+    _tensor(me, "y", y, 2, _FLOATS, (None, N // 2 if glu else N))
     size = w.element_size()
     a = GroupedArgs(E, n_rows, N, K, x_dtype, w_dtype, _FLOATS[y.dtype], 1 if glu else 0, _ptr(x),
                     _ptr(x_scales), ldx, x.shape[0], x_index_div, _ptr(x_index), _ptr(w), _ptr(w_scales),
@@ -459,13 +472,14 @@ def moe_combine_pairs(p, w, y, ids=None, n_experts=0, stream=None):
     """y [T, H] = sum over j of w[t, j] * p[t*k + j]; p [T*k, H], w f32 [T, k];
     with ids int32 [T, k], pairs outside 0..n_experts-1 are left out."""
     me = "moe_combine_pairs"
-    _tensor(me, "w", w, 2, (torch.float32,), contiguous=True)
+    _tensor(me, "w", w, 2, _F32, contiguous=True)
     T, k = w.shape
-    _tensor(me, "p", p, 2, tuple(_FLOATS), (T * k, None))
+    _tensor(me, "p", p, 2, _FLOATS)
+    _need(p.shape[0] == T * k, me, f"p: {p.shape[0]} rows, expected {T * k}")
     H = p.shape[1]
-    _tensor(me, "y", y, 2, tuple(_FLOATS), (T, H))
+    _tensor(me, "y", y, 2, _FLOATS, (T, H))
     if ids is not None:
-        _tensor(me, "ids", ids, 2, (torch.int32,), (T, k), True)
+        _tensor(me, "ids", ids, 2, _I32, (T, k), True)
     _call(me, lib().moe_combine_pairs, (p, w, y, ids), stream, _ptr(p), _FLOATS[p.dtype], _ld(p), _ptr(w),
           _ptr(ids), n_experts, T, k, H, _ptr(y), _FLOATS[y.dtype], _ld(y))
 

@@ -1,12 +1,14 @@
 // Products y = x W^T with bf16 or MXFP4 operands, dense or ragged by expert:
-// the variant for few rows, which streams weights.
+// the variant for few rows, and the choice between the variants.
 //
-// A workgroup of eight waves owns 16 rows of W (with GLU: 16 gate rows and the
-// matching 16 up rows) against a tile of up to 16*MI rows of x.  The waves
-// take K in turns of 128 elements, each lane loading its MFMA fragment straight
-// from memory (16 bytes of one row of W: 64 contiguous bytes per row and
-// load), so every weight byte is read once per tile and nothing waits at a
-// barrier until the waves' sums meet in LDS, in a fixed order.
+// A workgroup of eight waves owns 16*NB rows of W (with GLU: as many gate rows
+// and the matching up rows) against a tile of up to 16*MI rows of x, in 16x16
+// MFMA blocks.  The waves take K in turns of 128 elements, each lane loading
+// its fragments straight from memory (16 bytes of a row, four lanes 64
+// neighbouring bytes), the next turn's before the current one is multiplied;
+// nothing waits at a barrier until the waves' sums meet in LDS, in a fixed
+// order.  So even a product of one token keeps every CU's loads in flight, and
+// K costs a few memory latencies instead of one per step.
 //
 // W is the MFMA's first operand: a lane then holds four neighbouring columns of
 // one row of y.  The order of K inside a turn is the same for both operands
@@ -15,6 +17,8 @@
 //   bf16 x MXFP4    slice s, lane group g: k = 32g + 8s + [0,8): a lane's codes
 //                   are one 16-byte piece under one scale
 //   MXFP4 x MXFP4   lane group g: k = 32g + [0,32), the scaled MFMA's own order
+#include <type_traits>
+
 #include "ops.h"
 
 namespace moert {
@@ -22,14 +26,15 @@ namespace moert {
 constexpr int kSmWaves = 8;
 constexpr int kSmTurn = 128;  // elements of K per wave and turn
 
-template <int AT, int WT, bool GLU, int MI>
-__global__ __launch_bounds__(kSmWaves * 64) void product_small_kernel(ProductArgs a) {
-  constexpr int NB = GLU ? 2 : 1;
+template <int AT, int WT, bool GLU, int MI, int NB>
+__global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(ProductArgs a) {
+  constexpr int NW = GLU ? 2 * NB : NB;  // W blocks: gate blocks, then up blocks
   constexpr bool XM = AT == MOE_MXFP4, WM = WT == MOE_MXFP4;
-  __shared__ op_f32x4 s_red[kSmWaves / 2][MI * NB][64];
+  constexpr int CW = WM ? 1 : 4, CX = XM ? 1 : 4;  // 16-byte pieces per row and turn
+  __shared__ op_f32x4 s_red[kSmWaves / 2][MI * NW][64];
   const int n_out = GLU ? a.N / 2 : a.N;
-  const int n_blocks = (n_out + 15) >> 4;
-  const int nb = blockIdx.x % n_blocks;
+  const int n_blocks = (n_out + 16 * NB - 1) / (16 * NB);
+  const int n0 = (blockIdx.x % n_blocks) * (16 * NB);
   OpTile t;
   if (!OpTiles(a, MI * 16).find(a, MI * 16, blockIdx.x / n_blocks, &t)) return;
   const int lane = threadIdx.x & 63;
@@ -37,12 +42,13 @@ __global__ __launch_bounds__(kSmWaves * 64) void product_small_kernel(ProductArg
   const int r = lane & 15, g = lane >> 4;
   const int K = a.K;
 
-  const uint8_t* w[NB];
-  const uint8_t* ws[NB];
+  // rows of W past the end repeat the last one (their columns are not written),
+  // rows of x past the tile's end or without a source the first (nor are these)
+  const uint8_t* w[NW];
+  const uint8_t* ws[NW];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    // rows past the end repeat the last one; their columns are not written
-    const int64_t n = min(nb * 16 + r, n_out - 1) + b * n_out;
+  for (int b = 0; b < NW; ++b) {
+    const int64_t n = min(n0 + (b % NB) * 16 + r, n_out - 1) + (b / NB) * n_out;
     w[b] = a.w + (int64_t)t.e * a.w_stride + n * (WM ? K / 2 : K * 2);
     ws[b] = WM ? a.ws + (int64_t)t.e * a.ws_stride + n * (K / 32) : nullptr;
   }
@@ -58,73 +64,88 @@ __global__ __launch_bounds__(kSmWaves * 64) void product_small_kernel(ProductArg
     xs[i] = XM ? a.xs + (int64_t)max(row, 0) * (K / 32) : nullptr;
   }
 
-  op_f32x4 acc[MI][NB];
+  op_f32x4 acc[MI][NW];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) acc[i][b] = op_f32x4{};
-  const op_u32x4 zero = {0, 0, 0, 0};
+    for (int b = 0; b < NW; ++b) acc[i][b] = op_f32x4{};
 
-  for (int k0 = wave * kSmTurn; k0 < K; k0 += kSmWaves * kSmTurn) {
-    if constexpr (!WM) {
+  struct Turn {
+    op_u32x4 w[NW][CW], x[MI][CX];
+    uint32_t ws[NW], xs[MI];
+  };
+  // a lane's element of piece c in the turn at k0
+  auto at = [&](int k0, int c, bool codes) { return k0 + (codes ? 32 * g : WM ? 32 * g + 8 * c : 32 * c + 8 * g); };
+  auto load = [&](int k0, auto whole_c) {
+    constexpr bool whole = decltype(whole_c)::value;
+    Turn f;
+    const op_u32x4 zero = {0, 0, 0, 0};
+    // pieces past the end of a row become zeros (and their scales 1)
+    auto piece = [&](const uint8_t* row, int k, int bytes2) {
+      const bool in = whole || k < K;
+      const op_u32x4 v = *(const op_u32x4*)(row + (int64_t)(in ? k : 0) * bytes2 / 4);
+      return in ? v : zero;
+    };
+    auto scale = [&](const uint8_t* row) {
+      const int b = k0 / 32 + g;
+      const bool in = whole || b * 32 < K;
+      const uint32_t v = row[in ? b : 0];
+      return in ? v : 127u;
+    };
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int k = k0 + 32 * c + 8 * g;
-        op_u32x4 wf[NB];
+    for (int b = 0; b < NW; ++b) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) wf[b] = k < K ? *(const op_u32x4*)(w[b] + (int64_t)k * 2) : zero;
+      for (int c = 0; c < CW; ++c) f.w[b][c] = piece(w[b], at(k0, c, WM), WM ? 2 : 8);
+      if constexpr (WM) f.ws[b] = scale(ws[b]);
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+      for (int c = 0; c < CX; ++c) f.x[i][c] = piece(x[i], at(k0, c, XM), XM ? 2 : 8);
+      if constexpr (XM) f.xs[i] = scale(xs[i]);
+    }
+    return f;
+  };
+  auto multiply = [&](const Turn& f) {
+    if constexpr (XM) {
+#pragma unroll
+      for (int b = 0; b < NW; ++b) {
+        const op_i32x8 wv = {(int)f.w[b][0][0], (int)f.w[b][0][1], (int)f.w[b][0][2], (int)f.w[b][0][3], 0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-          const op_u32x4 xf = k < K && live[i] ? *(const op_u32x4*)(x[i] + (int64_t)k * 2) : zero;
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(op_bf16x8, wf[b]),
-                                                                __builtin_bit_cast(op_bf16x8, xf), acc[i][b], 0, 0, 0);
+          const op_i32x8 xv = {(int)f.x[i][0][0], (int)f.x[i][0][1], (int)f.x[i][0][2], (int)f.x[i][0][3], 0, 0, 0, 0};
+          acc[i][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv, acc[i][b], 4, 4, 0, (int)f.ws[b], 0,
+                                                                       (int)f.xs[i]);
         }
       }
     } else {
-      const int k = k0 + 32 * g;
-      const bool in = k < K;
-      op_u32x4 wf[NB];
-      uint32_t wsc[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        wf[b] = in ? *(const op_u32x4*)(w[b] + k / 2) : zero;
-        wsc[b] = in ? ws[b][k / 32] : 127;
-      }
-      if constexpr (XM) {
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int i = 0; i < MI; ++i) {
-          const bool on = in && live[i];
-          const op_u32x4 xf = on ? *(const op_u32x4*)(x[i] + k / 2) : zero;
-          const uint32_t xsc = on ? xs[i][k / 32] : 127;
-          const op_i32x8 xv = {(int)xf[0], (int)xf[1], (int)xf[2], (int)xf[3], 0, 0, 0, 0};
+        for (int b = 0; b < NW; ++b) {
+          op_bf16x8 wv;
+          if constexpr (WM) wv = op_fp4x8(f.w[b][0][c], op_scale(f.ws[b]));
+          else wv = __builtin_bit_cast(op_bf16x8, f.w[b][c]);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const op_i32x8 wv = {(int)wf[b][0], (int)wf[b][1], (int)wf[b][2], (int)wf[b][3], 0, 0, 0, 0};
-            acc[i][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wv, xv, acc[i][b], 4, 4, 0, (int)wsc[b], 0,
-                                                                         (int)xsc);
-          }
+          for (int i = 0; i < MI; ++i)
+            acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(op_bf16x8, f.x[i][c]), acc[i][b],
+                                                                0, 0, 0);
         }
-      } else {
-        op_bf16x8 wv[NB][4];
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int s = 0; s < 4; ++s) wv[b][s] = op_fp4x8(wf[b][s], op_scale(wsc[b]));
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const op_u32x4 xf = in && live[i] ? *(const op_u32x4*)(x[i] + (int64_t)(k + 8 * s) * 2) : zero;
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              acc[i][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[b][s], __builtin_bit_cast(op_bf16x8, xf),
-                                                                  acc[i][b], 0, 0, 0);
-          }
-      }
     }
+  };
+
+  int k0 = wave * kSmTurn;
+  constexpr int kNext = kSmWaves * kSmTurn;
+  if (k0 + kSmTurn <= K) {
+    Turn f = load(k0, std::true_type{});
+    for (k0 += kNext; k0 + kSmTurn <= K; k0 += kNext) {
+      const Turn n = load(k0, std::true_type{});
+      multiply(f);
+      f = n;
+    }
+    multiply(f);
   }
+  if (k0 < K) multiply(load(k0, std::false_type{}));
 
   // the waves' sums, halved three times: always the same order
 #pragma unroll
@@ -133,14 +154,14 @@ __global__ __launch_bounds__(kSmWaves * 64) void product_small_kernel(ProductArg
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) s_red[wave - half][i * NB + b][lane] = acc[i][b];
+        for (int b = 0; b < NW; ++b) s_red[wave - half][i * NW + b][lane] = acc[i][b];
     __syncthreads();
     if (wave < half)
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) acc[i][b] += s_red[wave][i * NB + b][lane];
-    __syncthreads();
+        for (int b = 0; b < NW; ++b) acc[i][b] += s_red[wave][i * NW + b][lane];
+    if (half > 1) __syncthreads();
   }
   if (wave) return;
 #pragma unroll
@@ -149,26 +170,35 @@ __global__ __launch_bounds__(kSmWaves * 64) void product_small_kernel(ProductArg
     const int row = m < t.rows ? op_y_row(a, t.pos0 + m) : -1;
     if (row < 0) continue;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = nb * 16 + 4 * g + q;
-      if (n >= n_out) continue;
-      const float z = GLU ? op_silu_mul(acc[i][0][q], acc[i][NB - 1][q]) : acc[i][0][q];
-      const float v = live[i] ? z : 0.f;
-      const int64_t at = (int64_t)row * a.ldy + n;
-      if (a.y_f32) ((float*)a.y)[at] = v;
-      else ((uint16_t*)a.y)[at] = op_bf16(v);
-    }
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = n0 + b * 16 + 4 * g + q;
+        if (n >= n_out) continue;
+        const float z = GLU ? op_silu_mul(acc[i][b][q], acc[i][b + NW - NB][q]) : acc[i][b][q];
+        const float v = live[i] ? z : 0.f;
+        const int64_t o = (int64_t)row * a.ldy + n;
+        if (a.y_f32) ((float*)a.y)[o] = v;
+        else ((uint16_t*)a.y)[o] = op_bf16(v);
+      }
   }
+}
+
+template <int AT, int WT, bool GLU, int MI, int NB>
+static hipError_t launch_small_as(const ProductArgs& a, hipStream_t s) {
+  const int64_t n_blocks = ((GLU ? a.N / 2 : a.N) + 16 * NB - 1) / (16 * NB);
+  const int64_t wgs = op_max_tiles(a, 16 * MI) * n_blocks;
+  if (wgs * kSmWaves * 64 >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+  return launch_op(product_small_kernel<AT, WT, GLU, MI, NB>, dim3((unsigned)wgs), dim3(kSmWaves * 64), s, a);
 }
 
 template <int AT, int WT, bool GLU>
 static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
-  const int64_t n_blocks = ((GLU ? a.N / 2 : a.N) + 15) / 16;
-  const bool few = a.n_rows <= 16 * (int64_t)a.n_experts;
-  const int64_t wgs = op_max_tiles(a, few ? 16 : 64) * n_blocks;
-  if (wgs * kSmWaves * 64 >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-  return launch_op(few ? product_small_kernel<AT, WT, GLU, 1> : product_small_kernel<AT, WT, GLU, 4>,
-                   dim3((unsigned)wgs), dim3(kSmWaves * 64), s, a);
+  const int groups = std::min(a.n_experts, a.n_rows);
+  const int avg = (a.n_rows + groups - 1) / groups;
+  if (avg <= 16) return launch_small_as<AT, WT, GLU, 1, 1>(a, s);
+  if (avg <= 32) return launch_small_as<AT, WT, GLU, 2, 2>(a, s);
+  return launch_small_as<AT, WT, GLU, 4, GLU ? 2 : 4>(a, s);
 }
 
 template <int AT, int WT>
@@ -176,7 +206,8 @@ static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
   // The tile kernel addresses the rows of x of a tile with 32-bit offsets and
   // reads MXFP4 scales 8 at a time.
   const bool tile_ok = a.x_ld < (1 << 23) && (AT != MOE_MXFP4 || a.K >= 256);
-  if (a.n_rows > 16 * (int64_t)a.n_experts && tile_ok) {
+  const int64_t n_tiles = (op_max_tiles(a, 256) * ((glu ? a.N * 2 : a.N) + 255)) / 256;
+  if (n_tiles >= 128 && a.n_rows > 32 * (int64_t)a.n_experts && tile_ok) {
     if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, s);
     else if constexpr (WT == MOE_MXFP4) return launch_tile_w4(a, glu, s);
     else return launch_tile_bf16(a, glu, s);
