@@ -48,10 +48,12 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 // x_dtype / w_dtype as in moe_grouped_gemm; hipErrorInvalidConfiguration when
 // the product needs more workgroups than a launch may have
 hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool glu, hipStream_t s);
-// its variant for many rows (product_tile.h), one source file per pair of types
-hipError_t launch_tile_bf16(const ProductArgs& a, bool glu, hipStream_t s);
-hipError_t launch_tile_w4(const ProductArgs& a, bool glu, hipStream_t s);
-hipError_t launch_tile_mx(const ProductArgs& a, bool glu, hipStream_t s);
+// its variants that stage tiles in LDS (product_tile.h), one source file per
+// pair of types
+enum class TileKind { kBig, kDeep, kShared };
+hipError_t launch_tile_bf16(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);
+hipError_t launch_tile_w4(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);
+hipError_t launch_tile_mx(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);
 size_t group_workspace(int64_t pairs, int E);
 hipError_t launch_group_pairs(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* perm,
                               int32_t* ws, hipStream_t s);
@@ -87,9 +89,10 @@ __device__ inline op_bf16x8 op_fp4x8(uint32_t raw, float scale) {
   return op_bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-// silu(g) * u.  exp(-g) overflows to infinity for g < -88 and the quotient
-// becomes a zero: the limit, for finite u.
-__device__ inline float op_silu_mul(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+// silu(g) * u.  exp(-g) overflows to infinity for g < -88 and its reciprocal
+// (1 ulp, a fraction of a correct division's instructions) becomes a zero: the
+// limit, for finite u.
+__device__ inline float op_silu_mul(float g, float u) { return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u; }
 
 struct OpTile {
   int e, pos0, rows;  // expert, first position, positions (1..BM)

@@ -196,21 +196,43 @@ template <int AT, int WT, bool GLU>
 static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
   const int groups = std::min(a.n_experts, a.n_rows);
   const int avg = (a.n_rows + groups - 1) / groups;
-  if (avg <= 16) return launch_small_as<AT, WT, GLU, 1, 1>(a, s);
-  if (avg <= 32) return launch_small_as<AT, WT, GLU, 2, 2>(a, s);
+  const int64_t n_blocks = ((GLU ? a.N / 2 : a.N) + 15) / 16;
+  // 16-row blocks while those of W still fill the chip's CUs once: 32 rows of
+  // 2048x768 bf16 take 5.3 us in 16 x 16 blocks and 7.6 in 32 x 32, 128 rows of
+  // 4096x4096 61 and 34 us (29.5 in 64 x 64)
+  if (avg <= 16 || op_max_tiles(a, 16) * n_blocks <= 512) return launch_small_as<AT, WT, GLU, 1, 1>(a, s);
+  if (avg <= 64 || op_max_tiles(a, 32) * n_blocks <= 512) return launch_small_as<AT, WT, GLU, 2, 2>(a, s);
   return launch_small_as<AT, WT, GLU, 4, GLU ? 2 : 4>(a, s);
 }
 
+// Which variant, by the tiles that a call can make at most (us, MI355X, small /
+// Mid / Big; "up" is a GLU product of N = 1536, K = 2048 over 128 experts with 8
+// per token):
+//   Mid wants 64 tiles (129 with W4, whose small variant is the faster): W4A4
+//   4096x4096 at 64, 128 rows 11.8 / 12.6, 16.8 / 12.5; bf16 at 128, 256 rows
+//   29.5 / 32.1, 38.7 / 31.9; W4 at 128, 256, 512 rows 23.6 / 28, 30.2 / 28,
+//   57.8 / 28; up at 1 and 8 tokens W4A4 8.2 / 10.0, 17.3 / 13.5.
+//   Big wants 128 tiles of its own and, in the mean, 192 rows an expert: W4A4
+//   4096x4096 at 1,024 rows 19.4 Mid, 39.4 Big; at 4,096 rows 81 Mid, 45.8 Big; up
+//   at 1,024, 2,048 and 4,096 tokens 63 / 110, 98 / 114, 160 / 142.
+//   Mid is Shared beyond 256 tiles, one per CU: W4A4 2048x768 over 128 experts at
+//   256 tokens 34 Shared, 55 Deep; 128x4096x4096 (64 tiles) 14.5 Shared, 12.5 Deep.
 template <int AT, int WT>
 static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
-  // The tile kernel addresses the rows of x of a tile with 32-bit offsets and
-  // reads MXFP4 scales 8 at a time.
-  const bool tile_ok = a.x_ld < (1 << 23) && (AT != MOE_MXFP4 || a.K >= 256);
-  const int64_t n_tiles = (op_max_tiles(a, 256) * ((glu ? a.N * 2 : a.N) + 255)) / 256;
-  if (n_tiles >= 128 && a.n_rows > 32 * (int64_t)a.n_experts && tile_ok) {
-    if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, s);
-    else if constexpr (WT == MOE_MXFP4) return launch_tile_w4(a, glu, s);
-    else return launch_tile_bf16(a, glu, s);
+  constexpr bool W4 = AT == MOE_BF16 && WT == MOE_MXFP4;
+  // the tile kernels address the rows of x of a tile with 32-bit offsets and
+  // read MXFP4 scales 16 at a time
+  if (a.x_ld < (1 << 23) && (WT != MOE_MXFP4 || a.K >= 512)) {
+    const int64_t n_out = glu ? a.N / 2 : a.N;
+    const int64_t mid = op_max_tiles(a, 64) * ((n_out + 127) / 128);
+    const int64_t big = op_max_tiles(a, 256) * ((n_out + (glu ? 127 : 255)) / (glu ? 128 : 256));
+    auto tile = [&](TileKind kind) {
+      if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, kind, s);
+      else if constexpr (WT == MOE_MXFP4) return launch_tile_w4(a, glu, kind, s);
+      else return launch_tile_bf16(a, glu, kind, s);
+    };
+    if (big >= 128 && a.n_rows >= 192 * (int64_t)a.n_experts) return tile(TileKind::kBig);
+    if (mid >= (W4 ? 129 : 64)) return tile(mid > 256 ? TileKind::kShared : TileKind::kDeep);
   }
   return glu ? launch_small<AT, WT, true>(a, s) : launch_small<AT, WT, false>(a, s);
 }

@@ -1,20 +1,20 @@
-// Products y = x W^T, dense or ragged by expert: the variant for many rows.
+// Products y = x W^T, dense or ragged by expert: the variants that stage tiles
+// of both operands in LDS.
 //
-// A workgroup of four waves owns a tile of up to 256 rows of x against 256
-// rows of W (with GLU: 128 gate rows and the matching 128 up rows), in
-// v_mfma 32x32 blocks with fp32 accumulation.  The waves stand side by side:
-// each takes all of the tile's rows by 64 rows of W, NI x 2 blocks with NI =
-// ceil(rows / 32), so a short last tile of an expert costs only the blocks it
-// fills and loads every wave alike.  Per block pair a wave reads (NI + 2)
-// fragments from LDS for 2 NI products, 0.63 at NI = 8.
+// A workgroup of four waves owns a tile of up to 32*MaxI rows of x against
+// 128*J rows of W (with GLU, J = 2: 128 gate rows and the matching 128 up rows),
+// in v_mfma 32x32 blocks with fp32 accumulation.  The waves stand side by
+// side: each takes all of the tile's rows by 32*J rows of W, NI x J blocks with
+// NI = ceil(rows / 32), so a short last tile of an expert costs only the blocks
+// it fills and loads every wave alike.
 //
-// K goes in steps of 128 bytes of a row (64 bf16, 256 MXFP4) through two LDS
-// stages.  Direct-to-LDS loads fill a stage one whole step before it is
-// needed; 16-byte pieces of a row are XOR-swizzled so that the fragment reads
-// of 32 rows spread over the banks.  Fragments are read one slice (a quarter
-// of a step) ahead of the products that use them, also across the one barrier
-// per step, which sits before a step's last slice: from there on every wave
-// has read the stage, so the loads of the step after next may overwrite it.
+// K goes in steps of 128 bytes of a row (64 bf16, 256 MXFP4) through a ring of
+// LDS stages that direct-to-LDS loads fill Stages - 1 steps ahead; 16-byte
+// pieces of a row are XOR-swizzled so that the fragment reads of 32 rows spread
+// over the banks.  Fragments are read one slice (a quarter of a step) ahead of
+// the products that use them, also across the one barrier per step, which sits
+// before a step's last slice: from there on every wave has read the stage, so
+// the next copies may overwrite it.
 //
 // W is the first MFMA operand: a lane holds, of one row of y, four neighbouring
 // columns at a time.  The result passes through LDS once more, so that rows
@@ -22,9 +22,20 @@
 //
 // Formats: bf16 x bf16 uses v_mfma_f32_32x32x16_bf16; MXFP4 x MXFP4 the scaled
 // v_mfma 32x32x64 on the codes as they are, each lane passing the scale of its
-// 32-element piece, held in registers (loaded one step ahead straight from
-// memory: 8 bytes of a row per step); bf16 x MXFP4 keeps W as codes in LDS and
-// expands a fragment with the scaled converts right before its products.
+// 32-element piece; bf16 x MXFP4 keeps W as codes in LDS and expands a fragment
+// with the scaled converts right before its products.
+//
+// Shapes.  Big, 256 x 256 with two stages: (NI + 2) fragment reads per 2 NI
+// products, 0.63 at NI = 8, leave LDS bandwidth for the copies.  Mid, 64 x 128
+// (GLU 64 x 256), for products whose big tiles would leave CUs without one; there
+// a step's products last less than a memory latency, which Deep hides with more
+// stages and Shared with more workgroups on a CU (at most 80 KB of LDS each; the
+// GLU shapes with two operands at full width do not get there).
+//
+// 4096 x 4096 x 4096 takes 45.8 us with MXFP4 operands (3.0 PFLOP/s; a step 1.9 us
+// against 0.85 us of products) and 113 us with bf16 (1.22 PFLOP/s; 1.25 at K =
+// 8192), bound by what the copies of all CUs together get: one tile alone on
+// the chip takes 1.5 and 1.15 us a step.
 #pragma once
 
 #include <type_traits>
@@ -33,17 +44,36 @@
 
 namespace moert {
 
-constexpr int kTlM = 256, kTlN = 256, kTlRow = 128;
+constexpr int kTlRow = 128;
 constexpr int kTlThreads = 256;
-constexpr int kTlStageA = kTlM * kTlRow;
+
+typedef unsigned int tile_bytes16 __attribute__((ext_vector_type(4), aligned(1)));
 
 template <int AT, int WT>
+struct TileBig {
+  static constexpr bool W4 = WT == MOE_MXFP4 && AT == MOE_BF16;
+  static constexpr int MaxI = 8, J = 2, Stages = W4 ? 3 : 2;
+  static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : W4 ? 64 : 48;
+};
+template <int AT, int WT, bool GLU, bool Deep>
+struct TileMid {
+  static constexpr int MaxI = 2, J = GLU ? 2 : 1;
+  static constexpr int Stages = WT == MOE_MXFP4 && AT == MOE_BF16 ? 3 : !Deep ? 2 : GLU ? 3 : 4;
+  static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : 64;
+};
+
+template <int AT, int WT, class C>
 struct TileShape {
   static constexpr bool XM = AT == MOE_MXFP4, WM = WT == MOE_MXFP4, W4 = WM && !XM;
-  static constexpr int K = XM ? 256 : 64;        // elements of a step
+  static constexpr int M = 32 * C::MaxI, N = 128 * C::J;
   static constexpr int WRow = W4 ? 32 : kTlRow;  // bytes of a W row per step
-  static constexpr int StageB = kTlN * WRow;
+  static constexpr int StageA = M * kTlRow, StageB = N * WRow, Stage = StageA + StageB;
   static constexpr int BLoads = StageB / 4096;   // per wave and step
+  static constexpr int ScalePitch = C::ScaleBytes + 8;  // 2 banks more than a multiple of 4
+  static constexpr int ScaleRows = XM ? M + N : WM ? N : 0;
+  static constexpr int ScaleTurns = (ScaleRows + kTlThreads - 1) / kTlThreads;
+  static constexpr int StepBlocks = XM ? 8 : 2;         // scales of a row per step
+  static constexpr int ChunkSteps = WM ? C::ScaleBytes / StepBlocks : 1;
 };
 
 // 16 bytes per lane from base + voff to LDS at lds + 16 * lane
@@ -51,34 +81,49 @@ __device__ inline void tile_copy16(const void* base, uint32_t voff, uint32_t lds
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                ::"v"(voff), "s"(base), "s"(lds) : "memory", "m0");
 }
-__device__ inline uint32_t tile_lds(const void* p) { return (uint32_t)(uintptr_t)p; }
+// an LDS address that is the same in every lane, as a scalar
+__device__ inline uint32_t tile_lds(const void* p) { return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p); }
 
 // place of 16-byte piece c of row r: two rows fill the 64 banks once, so the
 // key changes every second row
 __device__ inline int tile_at(int r, int c) { return r * kTlRow + ((c ^ ((r >> 1) & 7)) << 4); }
 
-template <int AT, int WT, bool GLU>
+// this wave's reads and all but its newest N copies are done, and every wave is here
+template <int N>
+__device__ inline void tile_sync() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(N) : "memory");
+}
+
+template <int AT, int WT, bool GLU, class C>
 __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs a) {
-  using S = TileShape<AT, WT>;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_a[2][kTlStageA];
-  __shared__ __attribute__((aligned(1024))) uint8_t s_b[2][S::StageB];
-  __shared__ int32_t s_y[kTlM];     // row of y per tile row, -1 = none
-  __shared__ uint8_t s_live[kTlM];  // 0: the product is a row of zeros
+  using S = TileShape<AT, WT, C>;
+  using std::integral_constant;
+  constexpr int J = C::J, Stages = C::Stages;
+  static_assert(!GLU || J == 2, "a wave holds the gate and the up block of its columns");
+  __shared__ __attribute__((aligned(1024))) uint8_t s_st[Stages * S::Stage];
+  __shared__ __attribute__((aligned(16))) uint8_t s_sc[16 + S::ScaleRows * S::ScalePitch];
+  __shared__ int32_t s_y[S::M];     // row of y per tile row, -1 = none
+  __shared__ uint8_t s_live[S::M];  // 0: the product is a row of zeros
 
   const int n_out = GLU ? a.N / 2 : a.N;
-  constexpr int NT = GLU ? kTlN / 2 : kTlN;
+  constexpr int NT = GLU ? S::N / 2 : S::N;
   const int n_ntiles = (n_out + NT - 1) / NT;
 
-  // XCD-aware order: workgroups go round-robin over the 8 XCDs; XCD i takes the
-  // i-th eighth of the M-tiles, in groups of four with the N-tiles outside,
-  // so what runs together on an XCD shares rows of x and of W in its L2
-  const OpTiles tiles(a, kTlM);
-  const int xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
-  const int per_xcd = (tiles.total + 7) >> 3;
-  const int grp = local / (4 * n_ntiles), rem = local - grp * 4 * n_ntiles;
-  const int ml = grp * 4 + (rem & 3), nt = rem >> 2;
+  // XCD-aware order: workgroups go round-robin over the 8 XCDs.  The tiles are
+  // listed in groups of four M-tiles with the N-tiles outside, and XCD i takes the
+  // i-th eighth of the list, so what runs together on an XCD shares rows of x and
+  // of W in its L2.  Workgroups without a tile come last: between others they
+  // would leave their turn of the shader engines empty (every fourth one with
+  // work put all work on a quarter of the CUs).
+  const OpTiles tiles(a, S::M);
+  const int per_xcd = (tiles.total * n_ntiles + 7) >> 3;  // the launch keeps this below 2^31
+  const int local = blockIdx.x >> 3, f = (blockIdx.x & 7) * per_xcd + local;
+  if (local >= per_xcd || f >= tiles.total * n_ntiles) return;
+  const int grp = f / (4 * n_ntiles), rem = f - grp * 4 * n_ntiles;
+  const int in_grp = min(4, tiles.total - grp * 4);
+  const int nt = rem / in_grp;
   OpTile t;
-  if (ml >= per_xcd || !tiles.find(a, kTlM, xcd * per_xcd + ml, &t)) return;
+  if (!tiles.find(a, S::M, grp * 4 + rem - nt * in_grp, &t)) return;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -86,19 +131,21 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
   const int K = a.K, blocks = K / 32;
   const int x_bytes = S::XM ? K / 2 : K * 2;
   const int steps = (x_bytes + kTlRow - 1) / kTlRow;
+  const int whole = x_bytes / kTlRow;  // steps that do not end inside
   const int n0 = nt * NT;
 
-  // every position's row of x once; a position without one, and the padding of
-  // a short tile, read the tile's first valid row instead
-  {
-    const int p = t.pos0 + tid;
+  if (tid < S::M) {
     const bool in = tid < t.rows;
-    s_y[tid] = in ? op_y_row(a, p) : -1;
-    s_live[tid] = in && op_x_row(a, p) >= 0;
+    s_y[tid] = in ? op_y_row(a, t.pos0 + tid) : -1;
+    s_live[tid] = in && op_x_row(a, t.pos0 + tid) >= 0;
   }
   // base of the tile's rows of x: the whole of x under an index (32-bit offsets),
-  // else the tile's first row
-  const uint8_t* x0 = a.x_index ? a.x : a.x + (int64_t)t.pos0 * a.x_ld;
+  // else the tile's first row.  The padding of a short tile, and positions
+  // without a row of x, read the first row.
+  const uint8_t* const x0 = a.x_index ? a.x : a.x + (int64_t)t.pos0 * a.x_ld;
+  const uint8_t* const w0 = a.w + (int64_t)t.e * a.w_stride;
+  const uint8_t* const xs0 = S::XM ? (a.x_index ? a.xs : a.xs + (int64_t)t.pos0 * blocks) : nullptr;
+  const uint8_t* const ws0 = S::WM ? a.ws + (int64_t)t.e * a.ws_stride : nullptr;
   auto x_row = [&](int m) {
     if (!a.x_index) return m < t.rows ? m : 0;
     return max(m < t.rows ? op_x_row(a, t.pos0 + m) : -1, 0);
@@ -111,6 +158,7 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
 
   auto run = [&](auto ni_c) {
     constexpr int NI = decltype(ni_c)::value;
+    constexpr int Group = NI + S::BLoads;  // copies of one wave per step
 
     // Copies.  A lane's piece is the same in every row it copies: 32 rows lie
     // between them, a multiple of the swizzle's period.
@@ -120,283 +168,387 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
 #pragma unroll
     for (int q = 0; q < NI; ++q)
       a_off[q] = (uint32_t)x_row((q * 4 + wave) * 8 + r8) * (uint32_t)a.x_ld + piece * 16;
-    const uint8_t* const w0 = a.w + (int64_t)t.e * a.w_stride;
     const int half = (lane & 1) ^ ((lane >> 4) & 1);  // W4: rows 8 apart share banks, their halves swap
 #pragma unroll
     for (int q = 0; q < S::BLoads; ++q)
       b_off[q] = S::W4 ? (uint32_t)w_row((q * 4 + wave) * 32 + (lane >> 1)) * (uint32_t)(K / 2) + half * 16
                        : (uint32_t)w_row((q * 4 + wave) * 8 + r8) * (uint32_t)x_bytes + piece * 16;
-
-    auto copy_a = [&](int kt, int buf) {
-      const uint8_t* xb = x0 + (int64_t)kt * kTlRow;
-#pragma unroll
-      for (int q = 0; q < NI; ++q) tile_copy16(xb, a_off[q], tile_lds(s_a[buf] + wave * 1024 + q * 4096));
+    auto st_a = [&](int buf) { return s_st + buf * S::Stage; };
+    auto st_b = [&](int buf) { return s_st + buf * S::Stage + S::StageA; };
+    // copy q of a wave's Group, x first
+    auto copy = [&](const uint8_t* xb, const uint8_t* wb, int buf, int q) {
+      if (q < NI) tile_copy16(xb, a_off[q], tile_lds(st_a(buf) + wave * 1024 + q * 4096));
+      else tile_copy16(wb, b_off[q - NI], tile_lds(st_b(buf) + wave * 1024 + (q - NI) * 4096));
     };
-    auto copy_b = [&](int kt, int buf) {
+    auto copy_some = [&](int kt, int buf, int from, int to) {
+      const uint8_t* xb = x0 + (int64_t)kt * kTlRow;
       const uint8_t* wb = w0 + (int64_t)kt * S::WRow;
 #pragma unroll
-      for (int q = 0; q < S::BLoads; ++q) tile_copy16(wb, b_off[q], tile_lds(s_b[buf] + wave * 1024 + q * 4096));
+      for (int q = 0; q < Group; ++q)
+        if (q >= from && q < to) copy(xb, wb, buf, q);
     };
+    auto issue = [&](int kt, int buf) { copy_some(kt, buf, 0, Group); };
     // a step that ends inside: pieces past the row's end become zeros
     auto issue_end = [&](int kt, int buf) {
       const op_u32x4 zero = {0, 0, 0, 0};
       const bool a_in = kt * kTlRow + piece * 16 < x_bytes;
       if (a_in) {
-        copy_a(kt, buf);
+        copy_some(kt, buf, 0, NI);
       } else {
 #pragma unroll
-        for (int q = 0; q < NI; ++q) *(op_u32x4*)(s_a[buf] + wave * 1024 + q * 4096 + lane * 16) = zero;
+        for (int q = 0; q < NI; ++q) *(op_u32x4*)(st_a(buf) + wave * 1024 + q * 4096 + lane * 16) = zero;
       }
       if (S::W4 ? kt * 2 + half < blocks : a_in) {
-        copy_b(kt, buf);
+        copy_some(kt, buf, NI, Group);
       } else {
 #pragma unroll
-        for (int q = 0; q < S::BLoads; ++q) *(op_u32x4*)(s_b[buf] + wave * 1024 + q * 4096 + lane * 16) = zero;
+        for (int q = 0; q < S::BLoads; ++q) *(op_u32x4*)(st_b(buf) + wave * 1024 + q * 4096 + lane * 16) = zero;
       }
     };
 
-    // this wave's W rows within the tile: blocks j = 0, 1
-    int brow[2];
+    // this lane's W rows within the tile
+    int brow[J];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) brow[j] = (GLU ? j * NT + wave * 32 : wave * 64 + j * 32) + lr;
+    for (int j = 0; j < J; ++j) brow[j] = (GLU ? j * NT + wave * 32 : wave * 32 * J + j * 32) + lr;
 
-    // scales: MXFP4 x MXFP4 8 bytes per row and step, shifted so that this
-    // half's blocks 2 ks + kg are bytes 0 and 2 of the two words; W4 one byte
-    uint2 sx[S::XM ? NI : 1], sw[2], sx_n[S::XM ? NI : 1], sw_n[2];
-    uint32_t sx_off[S::XM ? NI : 1], sw_off[2];
-    const uint8_t* const xs0 = S::XM ? (a.x_index ? a.xs : a.xs + (int64_t)t.pos0 * blocks) : nullptr;
-    const uint8_t* const ws0 = S::WM ? a.ws + (int64_t)t.e * a.ws_stride : nullptr;
-    if constexpr (S::XM)
+    // Scales lie in LDS for ChunkSteps steps at once (K >= 512): a row's scales of
+    // one step are 8 or 2 bytes, too few for a load each.  A thread brings whole
+    // rows, requested a step before they are needed.  The pieces of a row's end
+    // overlap the ones before; a row with less than 16 left reads into the past
+    // and writes that before its place, where nothing lies: the end of the
+    // previous row's place, which is unused then, or the 16 bytes in front.
+    constexpr int Pieces = C::ScaleBytes / 16;
+    tile_bytes16 sc[S::WM ? S::ScaleTurns * Pieces : 1];
+    const uint8_t* sc_src[S::WM ? S::ScaleTurns : 1];
+    if constexpr (S::WM) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) sx_off[i] = (uint32_t)x_row(i * 32 + lr) * (uint32_t)blocks;
-    if constexpr (S::WM)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) sw_off[j] = (uint32_t)w_row(brow[j]) * (uint32_t)blocks;
+      for (int u = 0; u < S::ScaleTurns; ++u) {
+        const int r = min(u * kTlThreads + tid, S::N + (S::XM ? NI * 32 : 0) - 1);
+        sc_src[u] = r < S::N ? ws0 + (uint32_t)w_row(r) * (uint32_t)blocks
+                             : xs0 + (uint32_t)x_row(r - S::N) * (uint32_t)blocks;
+      }
+    }
     auto load_scales = [&](int kt) {
-      if constexpr (S::XM) {
-        // the last step may end inside its 8 blocks: it reads the row's last 8
-        // and shifts them down below
-        const int b = min(kt * 8, blocks - 8);
+      if constexpr (S::WM) {
+        const int b0 = kt * S::StepBlocks, n = min(C::ScaleBytes, blocks - b0);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) __builtin_memcpy(&sx_n[i], xs0 + b + sx_off[i], 8);
+        for (int u = 0; u < S::ScaleTurns; ++u)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) __builtin_memcpy(&sw_n[j], ws0 + b + sw_off[j], 8);
-      } else if constexpr (S::W4) {
-        const int b = kt * 2 + kg;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) sw_n[j].x = b < blocks ? ws0[sw_off[j] + b] : 127;
+          for (int d = 0; d < Pieces; ++d)
+            sc[u * Pieces + d] = *(const tile_bytes16*)(sc_src[u] + b0 + min(d * 16, n - 16));
       }
     };
-    // claimed here, right after a wait for every load, so that the compiler's own
-    // wait for these loads does not fall behind the next stage's copies
-    auto take_scales = [&](int kt, bool whole_step) {
-      auto take = [&](uint2 v) {
-        asm volatile("" : "+v"(v.x), "+v"(v.y));
-        const int past = kt * 8 + 8 - blocks;  // blocks past the row's end: scale 1
-        if (!whole_step && past > 0) {         // (their codes are zeros, but zero times a NaN scale is not)
-          uint64_t d = (uint64_t)v.y << 32 | v.x;
-          d = d >> (8 * past) | 0x7F7F7F7F7F7F7F7Full << (64 - 8 * past);
-          v = make_uint2((uint32_t)d, (uint32_t)(d >> 32));
+    auto store_scales = [&](int kt) {
+      if constexpr (S::WM) {
+        const int n = min(C::ScaleBytes, blocks - kt * S::StepBlocks);
+#pragma unroll
+        for (int u = 0; u < S::ScaleTurns; ++u) {
+          const int r = u * kTlThreads + tid;
+          if (r < S::N + (S::XM ? NI * 32 : 0))
+#pragma unroll
+            for (int d = 0; d < Pieces; ++d)
+              *(tile_bytes16*)(s_sc + 16 + r * S::ScalePitch + min(d * 16, n - 16)) = sc[u * Pieces + d];
         }
-        return make_uint2(v.x >> (8 * kg), v.y >> (8 * kg));
-      };
+      }
+    };
+    // One step's: MXFP4 x MXFP4 the 8 of a row, shifted so that this half's
+    // blocks 2 ks + kg are bytes 0 and 2 of the two words, and those past the row's
+    // end 1 (their codes are zeros, but zero times a NaN scale is not); W4 that of
+    // block kg.
+    uint2 sx[S::XM ? NI : 1], sw[J], sx_n[S::XM ? NI : 1], sw_n[J];
+    auto read_scales = [&](int at) {  // at: offset of the step within the chunk
       if constexpr (S::XM) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) sx[i] = take(sx_n[i]);
+        for (int i = 0; i < NI; ++i) sx_n[i] = *(const uint2*)(s_sc + 16 + (S::N + i * 32 + lr) * S::ScalePitch + at);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sw[j] = take(sw_n[j]);
-      } else if constexpr (S::W4) {
+        for (int j = 0; j < J; ++j) sw_n[j] = *(const uint2*)(s_sc + 16 + brow[j] * S::ScalePitch + at);
+      } else if constexpr (S::WM) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          asm volatile("" : "+v"(sw_n[j].x));
-          sw[j].x = sw_n[j].x;
-        }
+        for (int j = 0; j < J; ++j) sw_n[j].x = s_sc[16 + brow[j] * S::ScalePitch + at + kg];
+      }
+    };
+    auto take_scales = [&](int kt, bool whole_step) {
+      if constexpr (S::XM) {
+        auto cut = [&](uint2 v) {
+          const int past = kt * 8 + 8 - blocks;
+          if (!whole_step && past > 0) {
+            uint64_t d = (uint64_t)v.y << 32 | v.x;
+            d = (d & ~0ull >> (8 * past)) | 0x7F7F7F7F7F7F7F7Full << (64 - 8 * past);
+            v = make_uint2((uint32_t)d, (uint32_t)(d >> 32));
+          }
+          return make_uint2(v.x >> (8 * kg), v.y >> (8 * kg));
+        };
+#pragma unroll
+        for (int i = 0; i < NI; ++i) sx[i] = cut(sx_n[i]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) sw[j] = cut(sw_n[j]);
+      } else if constexpr (S::WM) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) sw[j].x = whole_step || kt * 2 + kg < blocks ? sw_n[j].x : 127;
       }
     };
 
-    op_f32x16 acc[NI][2];
+    op_f32x16 acc[NI][J];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = op_f32x16{};
+      for (int j = 0; j < J; ++j) acc[i][j] = op_f32x16{};
 
     // fragments of slice ks: x piece 2 ks + kg of a row (W4: 4 kg + ks, so that
     // a lane's codes of a step are one piece under one scale)
-    op_u32x4 fx[2][NI], fw[2][2];
+    op_u32x4 fx[2][NI], fw[2][J];
     auto read = [&](int buf, int ks, int to) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        fx[to][i] = *(const op_u32x4*)(s_a[buf] + tile_at(i * 32 + lr, S::W4 ? 4 * kg + ks : 2 * ks + kg));
+        fx[to][i] = *(const op_u32x4*)(st_a(buf) + tile_at(i * 32 + lr, S::W4 ? 4 * kg + ks : 2 * ks + kg));
       if constexpr (!S::W4) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) fw[to][j] = *(const op_u32x4*)(s_b[buf] + tile_at(brow[j], 2 * ks + kg));
+        for (int j = 0; j < J; ++j) fw[to][j] = *(const op_u32x4*)(st_b(buf) + tile_at(brow[j], 2 * ks + kg));
       } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          fw[to][j][0] = *(const uint32_t*)(s_b[buf] + brow[j] * 32 + ((kg ^ ((brow[j] >> 3) & 1)) << 4) + ks * 4);
+        for (int j = 0; j < J; ++j)
+          fw[to][j][0] = *(const uint32_t*)(st_b(buf) + brow[j] * 32 + ((kg ^ ((brow[j] >> 3) & 1)) << 4) + ks * 4);
       }
     };
-    auto multiply = [&](auto ks_c, int from) {
+    // W fragments of a slice, ready for the MFMA
+    op_i32x8 wq[J];
+    op_bf16x8 wb[J];
+    auto unpack = [&](int from) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const op_u32x4 f = fw[from][j];
+        if constexpr (S::XM) wq[j] = op_i32x8{(int)f[0], (int)f[1], (int)f[2], (int)f[3], 0, 0, 0, 0};
+        else if constexpr (S::W4) wb[j] = op_fp4x8(f[0], op_scale(sw[j].x));
+        else wb[j] = __builtin_bit_cast(op_bf16x8, f);
+      }
+    };
+    // the products of row block i.  They have no side effects, and the compiler
+    // would sink them below the reads of later slices and the barrier, whose
+    // fragments then do not fit the registers, or move the reads down to their
+    // uses, each with its whole latency: the empty asm keeps a block's products
+    // where they stand.
+    auto block = [&](auto ks_c, int from, int i) {
       constexpr int ks = decltype(ks_c)::value;
-      if constexpr (S::XM) {
-        op_i32x8 wv[2];
+      const op_u32x4 f = fx[from][i];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          wv[j] = op_i32x8{(int)fw[from][j][0], (int)fw[from][j][1], (int)fw[from][j][2], (int)fw[from][j][3], 0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const op_i32x8 xv = {(int)fx[from][i][0], (int)fx[from][i][1], (int)fx[from][i][2], (int)fx[from][i][3], 0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-                wv[j], xv, acc[i][j], 4, 4, (ks & 1) * 2, (int)(ks < 2 ? sw[j].x : sw[j].y), (ks & 1) * 2,
-                (int)(ks < 2 ? sx[i].x : sx[i].y));
-        }
-      } else {
-        op_bf16x8 wv[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if constexpr (S::W4) wv[j] = op_fp4x8(fw[from][j][0], op_scale(sw[j].x));
-          else wv[j] = __builtin_bit_cast(op_bf16x8, fw[from][j]);
-        }
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv[j], __builtin_bit_cast(op_bf16x8, fx[from][i]),
-                                                                acc[i][j], 0, 0, 0);
+      for (int j = 0; j < J; ++j) {
+        if constexpr (S::XM)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              wq[j], op_i32x8{(int)f[0], (int)f[1], (int)f[2], (int)f[3], 0, 0, 0, 0}, acc[i][j], 4, 4, (ks & 1) * 2,
+              (int)(ks < 2 ? sw[j].x : sw[j].y), (ks & 1) * 2, (int)(ks < 2 ? sx[i].x : sx[i].y));
+        else
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], __builtin_bit_cast(op_bf16x8, f), acc[i][j], 0, 0, 0);
+        asm volatile("" : "+a"(acc[i][j]));
       }
     };
-    // Products have no side effects, and the compiler sinks the scaled ones below
-    // the step's barrier, past reads whose fragments then do not fit the
-    // registers: an empty asm on every sum keeps a slice's products in place.
-    auto hold = [&] {
-      if constexpr (S::XM) {
+    // a slice: the products of fragments `from` with the reads of the next slice
+    // woven in, one per product
+    auto slice = [&](auto ks_c, int buf, int from) {
+      constexpr int ks = decltype(ks_c)::value;
+      read(buf, ks + 1, from ^ 1);
+      unpack(from);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) asm volatile("" : "+a"(acc[i][0]), "+a"(acc[i][1]));
+      for (int i = 0; i < NI; ++i) block(ks_c, from, i);
+#pragma unroll
+      for (int n = 0; n < NI * J; ++n) {
+        if constexpr (NI * J < NI + J) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+        else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
       }
+      __builtin_amdgcn_sched_barrier(0);
     };
-    using std::integral_constant;
-    // one step on stage buf; slice 0 is in fragments 0.  steady: steps kt + 1 and
-    // kt + 2 exist and are whole
-    const int whole = x_bytes / kTlRow;
+    // One step on stage buf; slice 0 is in fragments 0.  steady: the next Stages
+    // steps exist and are whole, so exactly Stages - 2 groups of copies are
+    // newer than the next step's.
+    int sc_at = 0;  // of this step, within the chunk
     auto step = [&](int kt, int buf, auto steady_c) {
       constexpr bool steady = decltype(steady_c)::value;
       const bool more = steady || kt + 1 < steps;
-      if (more) load_scales(kt + 1);
-      read(buf, 1, 1);
-      multiply(integral_constant<int, 0>{}, 0);
-      hold();
-      read(buf, 2, 0);
-      multiply(integral_constant<int, 1>{}, 1);
-      hold();
-      read(buf, 3, 1);
-      multiply(integral_constant<int, 2>{}, 0);
-      hold();
+      const int next = Stages == 2 ? buf ^ 1 : buf + 1 == Stages ? 0 : buf + 1;
+      // the next step's scales begin a chunk: requested now, in LDS after the barrier
+      const bool chunk = S::WM && more && sc_at + S::StepBlocks == C::ScaleBytes;
+      if (chunk) load_scales(kt + 1);
+      slice(integral_constant<int, 0>{}, buf, 0);
+      slice(integral_constant<int, 1>{}, buf, 1);
+      slice(integral_constant<int, 2>{}, buf, 0);
+      const integral_constant<int, 3> last{};
       if (more) {
-        // this wave's copies into the other stage have landed and its reads of
-        // this one are done
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (steady || kt + 2 < whole) {
-          copy_a(kt + 2, buf);
-          copy_b(kt + 2, buf);
-        } else if (kt + 2 < steps) {
-          issue_end(kt + 2, buf);
+        if (steady) tile_sync<(Stages - 2) * Group>();
+        else tile_sync<0>();
+        if constexpr (S::WM) {
+          sc_at = chunk ? 0 : sc_at + S::StepBlocks;
+          if (chunk) {
+            store_scales(kt + 1);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          }
+          read_scales(sc_at);
         }
-        read(buf ^ 1, 0, 0);
+        read(next, 0, 0);
       }
-      multiply(integral_constant<int, 3>{}, 1);
+      unpack(1);
+      if (steady) {
+        // the copies between the products
+        const uint8_t* xb = x0 + (int64_t)(kt + Stages) * kTlRow;
+        const uint8_t* wb = w0 + (int64_t)(kt + Stages) * S::WRow;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          block(last, 1, i);
+#pragma unroll
+          for (int q = Group * i / NI; q < Group * (i + 1) / NI; ++q) copy(xb, wb, buf, q);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        if (kt + Stages < whole) issue(kt + Stages, buf);
+        else if (kt + Stages < steps) issue_end(kt + Stages, buf);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) block(last, 1, i);
+      }
       if (more) take_scales(kt + 1, steady);
     };
 
     load_scales(0);
-    for (int kt = 0; kt < min(steps, 2); ++kt) {
-      if (kt < whole) {
-        copy_a(kt, kt);
-        copy_b(kt, kt);
-      } else {
-        issue_end(kt, kt);
-      }
+    for (int kt = 0; kt < min(steps, Stages); ++kt) {
+      if (kt < whole) issue(kt, kt);
+      else issue_end(kt, kt);
     }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    store_scales(0);
+    tile_sync<0>();
+    read_scales(0);
     take_scales(0, false);
     read(0, 0, 0);
-    int kt = 0;
-    for (; kt + 3 < whole; kt += 2) {
-      step(kt, 0, std::true_type{});
-      step(kt + 1, 1, std::true_type{});
+    int kt = 0, buf = 0;
+    if constexpr (Stages == 2) {
+      for (; kt + 3 < whole; kt += 2) {
+        step(kt, 0, std::true_type{});
+        step(kt + 1, 1, std::true_type{});
+      }
+    } else {
+#pragma unroll 1
+      for (; kt + Stages < whole; ++kt) {
+        step(kt, buf, std::true_type{});
+        buf = buf + 1 == Stages ? 0 : buf + 1;
+      }
     }
 #pragma unroll 1
-    for (; kt < steps; ++kt) step(kt, kt & 1, std::false_type{});
+    for (; kt < steps; ++kt) {
+      step(kt, buf, std::false_type{});
+      buf = buf + 1 == Stages ? 0 : buf + 1;
+    }
 
     // Result.  Element r of a lane's block: row lr of x, W row 8 (r/4) + 4 kg +
-    // r%4.  32 rows at a time go through this wave's part of the first stage.
-    constexpr int CW = GLU ? 32 : 64, CS = CW + 4;  // columns of a wave, padded stride
-    constexpr int LPR = CW / 4, RPI = 64 / LPR;     // lanes per row, rows per pass
-    static_assert(4 * 32 * CS * 4 <= 2 * kTlStageA, "the staging fits the x stages");
+    // r%4.  32 rows at a time go through this wave's part of the stages; what is
+    // done to them on the way out is a rolled loop, since code that runs once per
+    // tile costs its instruction fetches.
+    constexpr int CW = GLU ? 32 : 32 * J, CS = 32 * J + 4;  // columns of y of a wave; padded stride
+    constexpr int LPR = CW / 8, RPI = 64 / LPR;             // lanes per row (8 columns each), rows per pass
+    static_assert(4 * 32 * CS * 4 <= Stages * S::Stage, "the staging fits the stages");
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every wave is done with the stages
-    float* const c = (float*)&s_a[0][0] + wave * (32 * CS);
-    const int c4 = (lane % LPR) * 4, rs = lane / LPR;
-    const int col = n0 + wave * CW + c4;
-    const bool wide = a.y_f32 ? (((uintptr_t)a.y & 15) | (a.ldy & 3)) == 0 : (((uintptr_t)a.y & 7) | (a.ldy & 3)) == 0;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-#pragma unroll
-      for (int j = 0; j < (GLU ? 1 : 2); ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          op_f32x4 v;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            v[u] = GLU ? op_silu_mul(acc[i][0][q * 4 + u], acc[i][1][q * 4 + u]) : acc[i][j][q * 4 + u];
-          *(op_f32x4*)&c[lr * CS + j * 32 + q * 8 + kg * 4] = v;
-        }
+    float* const c = (float*)s_st + wave * (32 * CS);
+    const int c8 = (lane % LPR) * 8, rs = lane / LPR;
+    const int col = n0 + wave * CW + c8;
+    const bool wide = (((uintptr_t)a.y & 15) | (a.ldy & (a.y_f32 ? 3 : 7))) == 0 && col + 8 <= n_out;
+    auto out = [&](int i) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's rows are in LDS
-#pragma unroll 2
+      op_f32x4 v[32 / RPI][2];
+      int row[32 / RPI];
+#pragma unroll
       for (int q = 0; q < 32 / RPI; ++q) {
         const int rl = q * RPI + rs, m = i * 32 + rl;
-        const int row = s_y[m];
-        op_f32x4 v = *(const op_f32x4*)&c[rl * CS + c4];
-        if (!s_live[m]) v = op_f32x4{0.f, 0.f, 0.f, 0.f};
-        if (row < 0) continue;
-        const int64_t at = (int64_t)row * a.ldy + col;
-        if (wide && col + 4 <= n_out) {
-          if (a.y_f32) *(op_f32x4*)((float*)a.y + at) = v;
-          else
-            *(uint2*)((uint16_t*)a.y + at) = make_uint2(op_bf16(v[0]) | (uint32_t)op_bf16(v[1]) << 16,
-                                                        op_bf16(v[2]) | (uint32_t)op_bf16(v[3]) << 16);
+        row[q] = s_y[m];
+        const bool live = s_live[m];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          op_f32x4 z = *(const op_f32x4*)&c[rl * CS + c8 + h * 4];
+          if constexpr (GLU) {
+            const op_f32x4 u = *(const op_f32x4*)&c[rl * CS + 32 + c8 + h * 4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) z[w] = op_silu_mul(z[w], u[w]);
+          }
+          v[q][h] = live ? z : op_f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 32 / RPI; ++q) {
+        if (row[q] < 0) continue;
+        const int64_t at = (int64_t)row[q] * a.ldy + col;
+        if (wide) {
+          if (a.y_f32) {
+            *(op_f32x4*)((float*)a.y + at) = v[q][0];
+            *(op_f32x4*)((float*)a.y + at + 4) = v[q][1];
+          } else {
+            op_u32x4 p;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              p[w] = op_bf16(v[q][w >> 1][(w & 1) * 2]) | (uint32_t)op_bf16(v[q][w >> 1][(w & 1) * 2 + 1]) << 16;
+            *(op_u32x4*)((uint16_t*)a.y + at) = p;
+          }
         } else {
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
+          for (int u = 0; u < 8; ++u)
             if (col + u < n_out) {
-              if (a.y_f32) ((float*)a.y)[at + u] = v[u];
-              else ((uint16_t*)a.y)[at + u] = op_bf16(v[u]);
+              if (a.y_f32) ((float*)a.y)[at + u] = v[q][u >> 2][u & 3];
+              else ((uint16_t*)a.y)[at + u] = op_bf16(v[q][u >> 2][u & 3]);
             }
         }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next 32 rows overwrite them
+    };
+    auto put = [&](const op_f32x16 (&z)[J]) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(op_f32x4*)&c[lr * CS + j * 32 + q * 8 + kg * 4] =
+              op_f32x4{z[j][q * 4], z[j][q * 4 + 1], z[j][q * 4 + 2], z[j][q * 4 + 3]};
+    };
+#pragma unroll 1
+    for (int i = 0; i < NI; ++i) {
+      // the sums lie in registers, which have no index: a chain of copies
+      // of which one is taken
+#pragma unroll
+      for (int u = 0; u < NI; ++u)
+        if (i == u) put(acc[u]);
+      out(i);
     }
   };
-  switch ((t.rows + 31) >> 5) {
-    case 1: run(std::integral_constant<int, 1>{}); break;
-    case 2: run(std::integral_constant<int, 2>{}); break;
-    case 3:
-    case 4: run(std::integral_constant<int, 4>{}); break;
-    case 5:
-    case 6: run(std::integral_constant<int, 6>{}); break;
-    default: run(std::integral_constant<int, 8>{}); break;
+  const int ni = (t.rows + 31) >> 5;
+  if constexpr (C::MaxI == 2) {
+    if (ni == 1) run(integral_constant<int, 1>{});
+    else run(integral_constant<int, 2>{});
+  } else {
+    switch (ni) {
+      case 1: run(integral_constant<int, 1>{}); break;
+      case 2: run(integral_constant<int, 2>{}); break;
+      case 3:
+      case 4: run(integral_constant<int, 4>{}); break;
+      case 5:
+      case 6: run(integral_constant<int, 6>{}); break;
+      default: run(integral_constant<int, 8>{}); break;
+    }
   }
 }
 
-template <int AT, int WT>
-hipError_t launch_tile(const ProductArgs& a, bool glu, hipStream_t s) {
-  const int n_out = glu ? a.N / 2 : a.N, nt = glu ? kTlN / 2 : kTlN;
+template <int AT, int WT, bool GLU, class C>
+hipError_t launch_tile_as(const ProductArgs& a, hipStream_t s) {
+  using S = TileShape<AT, WT, C>;
+  const int n_out = GLU ? a.N / 2 : a.N, nt = GLU ? S::N / 2 : S::N;
   const int64_t n_ntiles = (n_out + nt - 1) / nt;
-  const int64_t per_xcd = (op_max_tiles(a, kTlM) + 7) / 8;
-  const int64_t wgs = 8 * ((per_xcd + 3) / 4 * 4) * n_ntiles;
+  const int64_t wgs = (op_max_tiles(a, S::M) * n_ntiles + 7) / 8 * 8;
   if (wgs * kTlThreads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-  return launch_op(glu ? product_tile_kernel<AT, WT, true> : product_tile_kernel<AT, WT, false>,
-                   dim3((unsigned)wgs), dim3(kTlThreads), s, a);
+  return launch_op(product_tile_kernel<AT, WT, GLU, C>, dim3((unsigned)wgs), dim3(kTlThreads), s, a);
+}
+
+template <int AT, int WT>
+hipError_t launch_tile(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s) {
+  constexpr bool W4 = AT == MOE_BF16 && WT == MOE_MXFP4;
+  if (kind == TileKind::kBig)
+    return glu ? launch_tile_as<AT, WT, true, TileBig<AT, WT>>(a, s) : launch_tile_as<AT, WT, false, TileBig<AT, WT>>(a, s);
+  // W4's stages are small enough for both at once; the other formats' GLU
+  // tiles are too large to share a CU
+  if (glu) return launch_tile_as<AT, WT, true, TileMid<AT, WT, true, !W4>>(a, s);
+  if constexpr (!W4)
+    if (kind == TileKind::kDeep) return launch_tile_as<AT, WT, false, TileMid<AT, WT, false, true>>(a, s);
+  return launch_tile_as<AT, WT, false, TileMid<AT, WT, false, false>>(a, s);
 }
 
 }  // namespace moert
