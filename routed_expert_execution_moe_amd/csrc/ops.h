@@ -98,10 +98,23 @@ struct OpTile {
   int e, pos0, rows;  // expert, first position, positions (1..BM)
 };
 
+// inclusive prefix sum over the 64 lanes, by DPP: shifts within rows of 16, then
+// the last lane of a row (of two rows) onto the rows behind it
+__device__ inline int op_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
 // The BM-row tiles of all groups, expert by expert.  One wave on its own: lane
 // l counts the tiles of its E/64 experts and a wave scan orders them; every
-// lane then gets the total, and find() the t-th tile.  Offsets are clamped into
-// 0..n_rows, so bad ones cost results but no access out of range.
+// lane then gets the total, and find() the t-th tile: the lane that holds it,
+// then, its experts (at most 16) a lane each, the expert.  Offsets are clamped
+// into 0..n_rows, so bad ones cost results but no access out of range.
 struct OpTiles {
   int incl, mine, total;
 
@@ -121,12 +134,7 @@ struct OpTiles {
       int lo;
       if (e < a.n_experts) mine += (range(a, e, &lo) + BM - 1) / BM;
     }
-    incl = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int v = __shfl_up(incl, d);
-      if (lane >= d) incl += v;
-    }
+    incl = op_scan(mine);
     total = __builtin_amdgcn_readlane(incl, 63);
   }
 
@@ -140,19 +148,19 @@ struct OpTiles {
     const uint64_t past = __ballot(incl > t);
     if (!past) return false;
     const int owner = __builtin_ctzll(past), per = (a.n_experts + 63) >> 6;
-    int left = t - __builtin_amdgcn_readlane(incl - mine, owner);
-    for (int e = owner * per; e < a.n_experts; ++e) {
-      int lo;
-      const int n = range(a, e, &lo), tiles = (n + BM - 1) / BM;
-      if (left < tiles) {
-        out->e = e;
-        out->pos0 = lo + left * BM;
-        out->rows = min(BM, n - left * BM);
-        return true;
-      }
-      left -= tiles;
-    }
-    return false;
+    const int left = t - __builtin_amdgcn_readlane(incl - mine, owner);
+    const int lane = threadIdx.x & 63, e = owner * per + lane;
+    int lo = 0, n = 0;
+    if (lane < per && e < a.n_experts) n = range(a, e, &lo);
+    const int tiles = (n + BM - 1) / BM, upto = op_scan(tiles);
+    const uint64_t hit = __ballot(upto > left);
+    if (!hit) return false;  // offsets changed since they were counted
+    const int at = __builtin_ctzll(hit);
+    const int skip = (left - __builtin_amdgcn_readlane(upto - tiles, at)) * BM;
+    out->e = owner * per + at;
+    out->pos0 = __builtin_amdgcn_readlane(lo, at) + skip;
+    out->rows = min(BM, __builtin_amdgcn_readlane(n, at) - skip);
+    return true;
   }
 };
 

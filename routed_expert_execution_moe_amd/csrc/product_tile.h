@@ -8,8 +8,8 @@
 // NI = ceil(rows / 32), so a short last tile of an expert costs only the blocks
 // it fills and loads every wave alike.
 //
-// K goes in steps of 128 bytes of a row (64 bf16, 256 MXFP4) through a ring of
-// LDS stages that direct-to-LDS loads fill Stages - 1 steps ahead; 16-byte
+// K goes in steps of 128 or 64 bytes of a row (64 bf16 or 256 MXFP4 in 128)
+// through a ring of LDS stages that direct-to-LDS loads fill Stages - 1 steps ahead; 16-byte
 // pieces of a row are XOR-swizzled so that the fragment reads of 32 rows spread
 // over the banks.  Fragments are read one slice (a quarter of a step) ahead of
 // the products that use them, also across the one barrier per step, which sits
@@ -44,7 +44,6 @@
 
 namespace moert {
 
-constexpr int kTlRow = 128;
 constexpr int kTlThreads = 256;
 
 typedef unsigned int tile_bytes16 __attribute__((ext_vector_type(4), aligned(1)));
@@ -52,12 +51,14 @@ typedef unsigned int tile_bytes16 __attribute__((ext_vector_type(4), aligned(1))
 template <int AT, int WT>
 struct TileBig {
   static constexpr bool W4 = WT == MOE_MXFP4 && AT == MOE_BF16;
-  static constexpr int MaxI = 8, J = 2, Stages = W4 ? 3 : 2;
+  static constexpr int MaxI = 8, J = 2, Row = 128, Stages = W4 ? 3 : 2;
+  static constexpr bool Unroll = !W4;
   static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : W4 ? 64 : 48;
 };
 template <int AT, int WT, bool GLU, bool Deep>
 struct TileMid {
-  static constexpr int MaxI = 2, J = GLU ? 2 : 1;
+  static constexpr int MaxI = 2, J = GLU ? 2 : 1, Row = 128;
+  static constexpr bool Unroll = false;
   static constexpr int Stages = WT == MOE_MXFP4 && AT == MOE_BF16 ? 3 : !Deep ? 2 : GLU ? 3 : 4;
   static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : 64;
 };
@@ -66,13 +67,16 @@ template <int AT, int WT, class C>
 struct TileShape {
   static constexpr bool XM = AT == MOE_MXFP4, WM = WT == MOE_MXFP4, W4 = WM && !XM;
   static constexpr int M = 32 * C::MaxI, N = 128 * C::J;
-  static constexpr int WRow = W4 ? 32 : kTlRow;  // bytes of a W row per step
-  static constexpr int StageA = M * kTlRow, StageB = N * WRow, Stage = StageA + StageB;
-  static constexpr int BLoads = StageB / 4096;   // per wave and step
+  static constexpr int Row = C::Row, Slices = Row / 32, Parts = Row / 16;  // bytes, slices, 16-byte pieces of a row per step
+  static constexpr int WRow = W4 ? Row / 4 : Row;                         // bytes of a W row per step
+  static_assert(!W4 || Row == 128, "a W4 row's step is two pieces");
+  static constexpr int StageA = M * Row, StageB = N * WRow, Stage = StageA + StageB;
+  static constexpr int CopyRows = 1024 / Row;   // rows of one copy of a wave
+  static constexpr int BLoads = StageB / 4096;  // per wave and step
   static constexpr int ScalePitch = C::ScaleBytes + 8;  // 2 banks more than a multiple of 4
   static constexpr int ScaleRows = XM ? M + N : WM ? N : 0;
   static constexpr int ScaleTurns = (ScaleRows + kTlThreads - 1) / kTlThreads;
-  static constexpr int StepBlocks = XM ? 8 : 2;         // scales of a row per step
+  static constexpr int StepBlocks = XM ? Row / 16 : 2;   // scales of a row per step
   static constexpr int ChunkSteps = WM ? C::ScaleBytes / StepBlocks : 1;
 };
 
@@ -84,9 +88,13 @@ __device__ inline void tile_copy16(const void* base, uint32_t voff, uint32_t lds
 // an LDS address that is the same in every lane, as a scalar
 __device__ inline uint32_t tile_lds(const void* p) { return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p); }
 
-// place of 16-byte piece c of row r: two rows fill the 64 banks once, so the
-// key changes every second row
-__device__ inline int tile_at(int r, int c) { return r * kTlRow + ((c ^ ((r >> 1) & 7)) << 4); }
+// swizzle key of row r and place of its 16-byte piece c: two (four) rows of 128
+// (64) bytes fill the 64 banks once, so the key changes from one such group to
+// the next
+template <int Row>
+__device__ inline int tile_key(int r) { return Row == 128 ? (r >> 1) & 7 : (r >> 2) & 3; }
+template <int Row>
+__device__ inline int tile_at(int r, int c) { return r * Row + ((c ^ tile_key<Row>(r)) << 4); }
 
 // this wave's reads and all but its newest N copies are done, and every wave is here
 template <int N>
@@ -102,8 +110,8 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
   static_assert(!GLU || J == 2, "a wave holds the gate and the up block of its columns");
   __shared__ __attribute__((aligned(1024))) uint8_t s_st[Stages * S::Stage];
   __shared__ __attribute__((aligned(16))) uint8_t s_sc[16 + S::ScaleRows * S::ScalePitch];
-  __shared__ int32_t s_y[S::M];     // row of y per tile row, -1 = none
-  __shared__ uint8_t s_live[S::M];  // 0: the product is a row of zeros
+  __shared__ int32_t s_y[S::M];  // row of y per tile row, -1 = none
+  __shared__ int32_t s_x[S::M];  // row of x (from x0), -1 = none: the product is a row of zeros
 
   const int n_out = GLU ? a.N / 2 : a.N;
   constexpr int NT = GLU ? S::N / 2 : S::N;
@@ -130,15 +138,10 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
   const int lr = lane & 31, kg = lane >> 5;
   const int K = a.K, blocks = K / 32;
   const int x_bytes = S::XM ? K / 2 : K * 2;
-  const int steps = (x_bytes + kTlRow - 1) / kTlRow;
-  const int whole = x_bytes / kTlRow;  // steps that do not end inside
+  const int steps = (x_bytes + S::Row - 1) / S::Row;
+  const int whole = x_bytes / S::Row;  // steps that do not end inside
   const int n0 = nt * NT;
 
-  if (tid < S::M) {
-    const bool in = tid < t.rows;
-    s_y[tid] = in ? op_y_row(a, t.pos0 + tid) : -1;
-    s_live[tid] = in && op_x_row(a, t.pos0 + tid) >= 0;
-  }
   // base of the tile's rows of x: the whole of x under an index (32-bit offsets),
   // else the tile's first row.  The padding of a short tile, and positions
   // without a row of x, read the first row.
@@ -146,10 +149,13 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
   const uint8_t* const w0 = a.w + (int64_t)t.e * a.w_stride;
   const uint8_t* const xs0 = S::XM ? (a.x_index ? a.xs : a.xs + (int64_t)t.pos0 * blocks) : nullptr;
   const uint8_t* const ws0 = S::WM ? a.ws + (int64_t)t.e * a.ws_stride : nullptr;
-  auto x_row = [&](int m) {
-    if (!a.x_index) return m < t.rows ? m : 0;
-    return max(m < t.rows ? op_x_row(a, t.pos0 + m) : -1, 0);
-  };
+  if (tid < S::M) {
+    const bool in = tid < t.rows;
+    s_y[tid] = in ? op_y_row(a, t.pos0 + tid) : -1;
+    s_x[tid] = !in ? -1 : a.x_index ? op_x_row(a, t.pos0 + tid) : tid;
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  auto x_row = [&](int m) { return max(s_x[m], 0); };
   // row of W of tile row b, those past the end repeat the last one
   auto w_row = [&](int b) {
     if (GLU) return min(n0 + (b & (NT - 1)), n_out - 1) + (b >= NT ? n_out : 0);
@@ -158,30 +164,31 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
 
   auto run = [&](auto ni_c) {
     constexpr int NI = decltype(ni_c)::value;
-    constexpr int Group = NI + S::BLoads;  // copies of one wave per step
+    constexpr int ALoads = (NI * 32 + 4 * S::CopyRows - 1) / (4 * S::CopyRows);
+    constexpr int Group = ALoads + S::BLoads;  // copies of one wave per step
 
-    // Copies.  A lane's piece is the same in every row it copies: 32 rows lie
-    // between them, a multiple of the swizzle's period.
-    const int r8 = lane >> 3;
-    const int piece = (lane & 7) ^ (((wave * 8 + r8) >> 1) & 7);
-    uint32_t a_off[NI], b_off[S::BLoads];
+    // Copies.  A lane's piece is the same in every row it copies: 4 CopyRows rows
+    // lie between them, a multiple of the swizzle's period.
+    const int cr = lane / S::Parts;
+    const int piece = (lane % S::Parts) ^ tile_key<S::Row>(wave * S::CopyRows + cr);
+    uint32_t a_off[ALoads], b_off[S::BLoads];
 #pragma unroll
-    for (int q = 0; q < NI; ++q)
-      a_off[q] = (uint32_t)x_row((q * 4 + wave) * 8 + r8) * (uint32_t)a.x_ld + piece * 16;
+    for (int q = 0; q < ALoads; ++q)
+      a_off[q] = (uint32_t)x_row((q * 4 + wave) * S::CopyRows + cr) * (uint32_t)a.x_ld + piece * 16;
     const int half = (lane & 1) ^ ((lane >> 4) & 1);  // W4: rows 8 apart share banks, their halves swap
 #pragma unroll
     for (int q = 0; q < S::BLoads; ++q)
       b_off[q] = S::W4 ? (uint32_t)w_row((q * 4 + wave) * 32 + (lane >> 1)) * (uint32_t)(K / 2) + half * 16
-                       : (uint32_t)w_row((q * 4 + wave) * 8 + r8) * (uint32_t)x_bytes + piece * 16;
+                       : (uint32_t)w_row((q * 4 + wave) * S::CopyRows + cr) * (uint32_t)x_bytes + piece * 16;
     auto st_a = [&](int buf) { return s_st + buf * S::Stage; };
     auto st_b = [&](int buf) { return s_st + buf * S::Stage + S::StageA; };
     // copy q of a wave's Group, x first
     auto copy = [&](const uint8_t* xb, const uint8_t* wb, int buf, int q) {
-      if (q < NI) tile_copy16(xb, a_off[q], tile_lds(st_a(buf) + wave * 1024 + q * 4096));
-      else tile_copy16(wb, b_off[q - NI], tile_lds(st_b(buf) + wave * 1024 + (q - NI) * 4096));
+      if (q < ALoads) tile_copy16(xb, a_off[q], tile_lds(st_a(buf) + wave * 1024 + q * 4096));
+      else tile_copy16(wb, b_off[q - ALoads], tile_lds(st_b(buf) + wave * 1024 + (q - ALoads) * 4096));
     };
     auto copy_some = [&](int kt, int buf, int from, int to) {
-      const uint8_t* xb = x0 + (int64_t)kt * kTlRow;
+      const uint8_t* xb = x0 + (int64_t)kt * S::Row;
       const uint8_t* wb = w0 + (int64_t)kt * S::WRow;
 #pragma unroll
       for (int q = 0; q < Group; ++q)
@@ -191,15 +198,15 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     // a step that ends inside: pieces past the row's end become zeros
     auto issue_end = [&](int kt, int buf) {
       const op_u32x4 zero = {0, 0, 0, 0};
-      const bool a_in = kt * kTlRow + piece * 16 < x_bytes;
+      const bool a_in = kt * S::Row + piece * 16 < x_bytes;
       if (a_in) {
-        copy_some(kt, buf, 0, NI);
+        copy_some(kt, buf, 0, ALoads);
       } else {
 #pragma unroll
-        for (int q = 0; q < NI; ++q) *(op_u32x4*)(st_a(buf) + wave * 1024 + q * 4096 + lane * 16) = zero;
+        for (int q = 0; q < ALoads; ++q) *(op_u32x4*)(st_a(buf) + wave * 1024 + q * 4096 + lane * 16) = zero;
       }
       if (S::W4 ? kt * 2 + half < blocks : a_in) {
-        copy_some(kt, buf, NI, Group);
+        copy_some(kt, buf, ALoads, Group);
       } else {
 #pragma unroll
         for (int q = 0; q < S::BLoads; ++q) *(op_u32x4*)(st_b(buf) + wave * 1024 + q * 4096 + lane * 16) = zero;
@@ -212,7 +219,7 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     for (int j = 0; j < J; ++j) brow[j] = (GLU ? j * NT + wave * 32 : wave * 32 * J + j * 32) + lr;
 
     // Scales lie in LDS for ChunkSteps steps at once (K >= 512): a row's scales of
-    // one step are 8 or 2 bytes, too few for a load each.  A thread brings whole
+    // one step are 2 to 8 bytes, too few for a load each.  A thread brings whole
     // rows, requested a step before they are needed.  The pieces of a row's end
     // overlap the ones before; a row with less than 16 left reads into the past
     // and writes that before its place, where nothing lies: the end of the
@@ -251,17 +258,22 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
         }
       }
     };
-    // One step's: MXFP4 x MXFP4 the 8 of a row, shifted so that this half's
-    // blocks 2 ks + kg are bytes 0 and 2 of the two words, and those past the row's
+    // One step's: MXFP4 x MXFP4 the 8 (4) of a row, shifted so that this half's
+    // blocks 2 ks + kg are bytes 0 and 2 of each word, and those past the row's
     // end 1 (their codes are zeros, but zero times a NaN scale is not); W4 that of
     // block kg.
     uint2 sx[S::XM ? NI : 1], sw[J], sx_n[S::XM ? NI : 1], sw_n[J];
     auto read_scales = [&](int at) {  // at: offset of the step within the chunk
       if constexpr (S::XM) {
+        auto get = [&](int r) {
+          const uint8_t* p = s_sc + 16 + r * S::ScalePitch + at;
+          if constexpr (S::Slices == 2) return make_uint2(*(const uint32_t*)p, 0);
+          else return *(const uint2*)p;
+        };
 #pragma unroll
-        for (int i = 0; i < NI; ++i) sx_n[i] = *(const uint2*)(s_sc + 16 + (S::N + i * 32 + lr) * S::ScalePitch + at);
+        for (int i = 0; i < NI; ++i) sx_n[i] = get(S::N + i * 32 + lr);
 #pragma unroll
-        for (int j = 0; j < J; ++j) sw_n[j] = *(const uint2*)(s_sc + 16 + brow[j] * S::ScalePitch + at);
+        for (int j = 0; j < J; ++j) sw_n[j] = get(brow[j]);
       } else if constexpr (S::WM) {
 #pragma unroll
         for (int j = 0; j < J; ++j) sw_n[j].x = s_sc[16 + brow[j] * S::ScalePitch + at + kg];
@@ -270,10 +282,11 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     auto take_scales = [&](int kt, bool whole_step) {
       if constexpr (S::XM) {
         auto cut = [&](uint2 v) {
-          const int past = kt * 8 + 8 - blocks;
+          const int past = (kt + 1) * S::StepBlocks - blocks;
           if (!whole_step && past > 0) {
-            uint64_t d = (uint64_t)v.y << 32 | v.x;
-            d = (d & ~0ull >> (8 * past)) | 0x7F7F7F7F7F7F7F7Full << (64 - 8 * past);
+            const int left = S::StepBlocks - past;  // 1 .. StepBlocks - 1
+            const uint64_t keep = ~0ull >> (64 - 8 * left);
+            const uint64_t d = (((uint64_t)v.y << 32 | v.x) & keep) | (0x7F7F7F7F7F7F7F7Full & ~keep);
             v = make_uint2((uint32_t)d, (uint32_t)(d >> 32));
           }
           return make_uint2(v.x >> (8 * kg), v.y >> (8 * kg));
@@ -300,10 +313,10 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     auto read = [&](int buf, int ks, int to) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        fx[to][i] = *(const op_u32x4*)(st_a(buf) + tile_at(i * 32 + lr, S::W4 ? 4 * kg + ks : 2 * ks + kg));
+        fx[to][i] = *(const op_u32x4*)(st_a(buf) + tile_at<S::Row>(i * 32 + lr, S::W4 ? 4 * kg + ks : 2 * ks + kg));
       if constexpr (!S::W4) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) fw[to][j] = *(const op_u32x4*)(st_b(buf) + tile_at(brow[j], 2 * ks + kg));
+        for (int j = 0; j < J; ++j) fw[to][j] = *(const op_u32x4*)(st_b(buf) + tile_at<S::Row>(brow[j], 2 * ks + kg));
       } else {
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -341,17 +354,21 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
         asm volatile("" : "+a"(acc[i][j]));
       }
     };
+    int sc_at = 0;  // offset of this step's scales within the chunk
     // a slice: the products of fragments `from` with the reads of the next slice
     // woven in, one per product
     auto slice = [&](auto ks_c, int buf, int from) {
       constexpr int ks = decltype(ks_c)::value;
       read(buf, ks + 1, from ^ 1);
+      // the next step's scales; where they begin a chunk, read again below
+      if constexpr (ks == 0 && S::WM) read_scales(sc_at + S::StepBlocks);
+      constexpr int reads = NI + J + (ks == 0 && S::WM ? (S::XM ? NI + J : J) : 0);
       unpack(from);
 #pragma unroll
       for (int i = 0; i < NI; ++i) block(ks_c, from, i);
 #pragma unroll
       for (int n = 0; n < NI * J; ++n) {
-        if constexpr (NI * J < NI + J) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+        if constexpr (NI * J < reads) __builtin_amdgcn_sched_group_barrier(0x100, (reads + NI * J - 1) / (NI * J), 0);  // LDS reads
         else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
       }
@@ -360,18 +377,19 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     // One step on stage buf; slice 0 is in fragments 0.  steady: the next Stages
     // steps exist and are whole, so exactly Stages - 2 groups of copies are
     // newer than the next step's.
-    int sc_at = 0;  // of this step, within the chunk
     auto step = [&](int kt, int buf, auto steady_c) {
       constexpr bool steady = decltype(steady_c)::value;
       const bool more = steady || kt + 1 < steps;
-      const int next = Stages == 2 ? buf ^ 1 : buf + 1 == Stages ? 0 : buf + 1;
+      const int next = buf + 1 == Stages ? 0 : buf + 1;
       // the next step's scales begin a chunk: requested now, in LDS after the barrier
       const bool chunk = S::WM && more && sc_at + S::StepBlocks == C::ScaleBytes;
       if (chunk) load_scales(kt + 1);
       slice(integral_constant<int, 0>{}, buf, 0);
-      slice(integral_constant<int, 1>{}, buf, 1);
-      slice(integral_constant<int, 2>{}, buf, 0);
-      const integral_constant<int, 3> last{};
+      if constexpr (S::Slices == 4) {
+        slice(integral_constant<int, 1>{}, buf, 1);
+        slice(integral_constant<int, 2>{}, buf, 0);
+      }
+      const integral_constant<int, S::Slices - 1> last{};
       if (more) {
         if (steady) tile_sync<(Stages - 2) * Group>();
         else tile_sync<0>();
@@ -380,15 +398,16 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
           if (chunk) {
             store_scales(kt + 1);
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            read_scales(0);
           }
-          read_scales(sc_at);
         }
         read(next, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);  // requested before the products, not after
       }
       unpack(1);
       if (steady) {
         // the copies between the products
-        const uint8_t* xb = x0 + (int64_t)(kt + Stages) * kTlRow;
+        const uint8_t* xb = x0 + (int64_t)(kt + Stages) * S::Row;
         const uint8_t* wb = w0 + (int64_t)(kt + Stages) * S::WRow;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -406,22 +425,25 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
       if (more) take_scales(kt + 1, steady);
     };
 
-    load_scales(0);
-    for (int kt = 0; kt < min(steps, Stages); ++kt) {
+    auto begin = [&](int kt) {
       if (kt < whole) issue(kt, kt);
-      else issue_end(kt, kt);
-    }
+      else if (kt < steps) issue_end(kt, kt);
+    };
+    begin(0);
+    load_scales(0);
     store_scales(0);
-    tile_sync<0>();
+#pragma unroll
+    for (int kt = 1; kt < Stages; ++kt) begin(kt);
+    if (whole >= Stages) tile_sync<(Stages - 1) * Group>();
+    else tile_sync<0>();
     read_scales(0);
     take_scales(0, false);
     read(0, 0, 0);
     int kt = 0, buf = 0;
-    if constexpr (Stages == 2) {
-      for (; kt + 3 < whole; kt += 2) {
-        step(kt, 0, std::true_type{});
-        step(kt + 1, 1, std::true_type{});
-      }
+    if constexpr (C::Unroll) {  // stages at fixed addresses
+      for (; kt + 2 * Stages - 1 < whole; kt += Stages)
+#pragma unroll
+        for (int u = 0; u < Stages; ++u) step(kt + u, u, std::true_type{});
     } else {
 #pragma unroll 1
       for (; kt + Stages < whole; ++kt) {
@@ -443,19 +465,17 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     constexpr int LPR = CW / 8, RPI = 64 / LPR;             // lanes per row (8 columns each), rows per pass
     static_assert(4 * 32 * CS * 4 <= Stages * S::Stage, "the staging fits the stages");
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every wave is done with the stages
-    float* const c = (float*)s_st + wave * (32 * CS);
     const int c8 = (lane % LPR) * 8, rs = lane / LPR;
     const int col = n0 + wave * CW + c8;
     const bool wide = (((uintptr_t)a.y & 15) | (a.ldy & (a.y_f32 ? 3 : 7))) == 0 && col + 8 <= n_out;
-    auto out = [&](int i) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's rows are in LDS
+    auto out = [&](int i, const float* c) {
       op_f32x4 v[32 / RPI][2];
       int row[32 / RPI];
 #pragma unroll
       for (int q = 0; q < 32 / RPI; ++q) {
         const int rl = q * RPI + rs, m = i * 32 + rl;
         row[q] = s_y[m];
-        const bool live = s_live[m];
+        const bool live = s_x[m] >= 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           op_f32x4 z = *(const op_f32x4*)&c[rl * CS + c8 + h * 4];
@@ -491,9 +511,8 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
             }
         }
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next 32 rows overwrite them
     };
-    auto put = [&](const op_f32x16 (&z)[J]) {
+    auto put = [&](const op_f32x16 (&z)[J], float* c) {
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -501,14 +520,22 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
           *(op_f32x4*)&c[lr * CS + j * 32 + q * 8 + kg * 4] =
               op_f32x4{z[j][q * 4], z[j][q * 4 + 1], z[j][q * 4 + 2], z[j][q * 4 + 3]};
     };
+    // as many row blocks at once as the stages hold, up to two: one round of
+    // latencies for both
+    constexpr int Batch = NI % 2 == 0 && 4 * 2 * 32 * CS * 4 <= Stages * S::Stage ? 2 : 1;
+    float* const c = (float*)s_st + wave * (Batch * 32 * CS);
 #pragma unroll 1
-    for (int i = 0; i < NI; ++i) {
-      // the sums lie in registers, which have no index: a chain of copies
-      // of which one is taken
+    for (int i = 0; i < NI; i += Batch) {
+      // the sums lie in registers, which have no index: one of the copies is taken
 #pragma unroll
-      for (int u = 0; u < NI; ++u)
-        if (i == u) put(acc[u]);
-      out(i);
+      for (int u = 0; u < NI; u += Batch)
+        if (i == u)
+#pragma unroll
+          for (int h = 0; h < Batch; ++h) put(acc[u + h], c + h * 32 * CS);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's rows are in LDS
+#pragma unroll
+      for (int h = 0; h < Batch; ++h) out(i + h, c + h * 32 * CS);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next rows overwrite them
     }
   };
   const int ni = (t.rows + 31) >> 5;

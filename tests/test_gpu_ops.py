@@ -194,6 +194,39 @@ def test_mx_gemm(t, B, M, N, K, act, out):
     _close(y, want, _bound(size, want, K, False), out == "bfloat16", (M, N, K))
 
 
+GEMM_TILES = [  # enough tiles for each of the LDS variants; ends inside steps and scale chunks
+    (500, 1100, 544), (500, 1100, 1600), (129, 4100, 2080),           # 64 x 128 tiles, one per CU
+    (1500, 1500, 672), (1090, 2050, 2112),                           # 64 x 128 tiles, several per CU
+    (2050, 4100, 544), (2049, 4353, 1568), (2300, 4000, 4192),       # 256 x 256 tiles
+]
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("M,N,K", GEMM_TILES)
+def test_mx_gemm_tiles(t, B, M, N, K, act):
+    log(f"gemm tiles {M}x{N}x{K} {act}")
+    rng = np.random.default_rng(M + N + K)
+    x, w = Operand(t, rng, M, K, act), Operand(t, rng, N, K, "mxfp4", 0.05)
+    if act == "mxfp4":
+        x.scales[5, -1] = 255  # the last block of a row: its steps end right behind it
+    w.scales[7, -1] = 255
+    want = t.from_numpy(x.v).cuda() @ t.from_numpy(w.v).cuda().T
+    size = t.from_numpy(np.abs(x.v)).cuda() @ t.from_numpy(np.abs(w.v)).cuda().T
+    for out in (t.float32, t.bfloat16):
+        y = t.full((M, N + 5), 7.0, dtype=out, device="cuda")
+        B.moe_mx_gemm(x.t, w.t, w.scales, y[:, :N], x_scales=x.scales)
+        t.cuda.synchronize()
+        tol = K * 2.0 ** -23 * size + (2.0 ** -8 * (want.abs() + K * 2.0 ** -23 * size) if out == t.bfloat16 else 2.0 ** -24 * want.abs())
+        bad = ~((y[:, :N].double() - want).abs() <= tol)
+        nan = t.zeros_like(bad)
+        nan[:, 7] = True
+        if act == "mxfp4":
+            nan[5] = True
+        assert bool((y[:, :N].isnan() == nan).all())
+        assert not bool((bad & ~nan).any()), t.nonzero(bad & ~nan)[:4].tolist()
+        assert bool((y[:, N:] == 7).all())
+
+
 @pytest.mark.parametrize("M", [3, 150])
 def test_mx_gemm_strides_and_alignment(t, B, M):
     """x rows inside a wider buffer; y rows of odd stride at an odd element;
@@ -335,6 +368,51 @@ def test_grouped_up_and_down(t, B, T, k, E, N, K, fmt):
         _close(y[_dev(t, live.astype(np.int64))], want[:n], _bound(size, want, K, False)[:n], out == "bfloat16", "down")
         dead = np.setdiff1d(np.arange(R), live)
         assert bool((y[_dev(t, dead)] == 7).all())
+
+
+GROUPED_TILES = [  # T, k, E, N, K, glu
+    (260, 4, 16, 1538, 544, True), (260, 4, 16, 1538, 544, False), (90, 8, 60, 2050, 1120, False),
+    (1500, 2, 5, 2050, 1568, True), (1500, 2, 5, 4098, 544, False), (3001, 3, 6, 1026, 2080, True),
+]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,k,E,N,K,glu", GROUPED_TILES)
+def test_grouped_tiles(t, B, T, k, E, N, K, glu, fmt):
+    """The LDS variants on ragged groups, odd columns, a row of x that no
+    position may mix with and positions without a source; compared on the GPU in
+    fp64."""
+    log(f"grouped tiles T={T} k={k} E={E} N={N} K={K} glu={glu} {fmt}")
+    act, wt = fmt.split("-")
+    rng = np.random.default_rng(T + N + K)
+    ids = _ids(rng, T, k, E, pad=T // 9)
+    ids[ids == 1] = 2  # an expert without rows
+    off, perm = OO.group_pairs(ids, E)
+    R, n = T * k, int(off[-1])
+    w, x = Experts(t, rng, E, N, K, wt), Operand(t, rng, T, K, act)
+    index = perm.copy()
+    index[3:n:41] = -1
+    cols = N // 2 if glu else N
+    xv = t.from_numpy(x.v).cuda()
+    want, size = t.zeros(R, cols, dtype=t.float64, device="cuda"), t.zeros(R, cols, dtype=t.float64, device="cuda")
+    for e in range(E):
+        p = np.arange(off[e], off[e + 1])
+        if len(p):
+            a = xv[_dev(t, np.maximum(index[p], 0) // k)] * _dev(t, (index[p] >= 0).astype(np.float64))[:, None]
+            we = t.from_numpy(w(e)).cuda()
+            z, m = a @ we.T, a.abs() @ we.abs().T
+            if glu:
+                g, u, mg, mu = z[:, :cols], z[:, cols:], m[:, :cols], m[:, cols:]
+                s = g * t.sigmoid(g)
+                z, m = s * u, 1.1 * mg * u.abs() + s.abs() * mu + 1e-3 * mg * mu
+            want[off[e]:off[e + 1]], size[off[e]:off[e + 1]] = z, m
+    tol = K * 2.0 ** -23 * size + (2e-5 * want.abs() if glu else 0)
+    for out in ("float32", "bfloat16"):
+        y = _grouped(t, B, x, w, off, R, N, out, x_index=index, div=k, glu=glu)
+        half = 2.0 ** -8 if out == "bfloat16" else 2.0 ** -24
+        bad = ~((y.double() - want).abs() <= tol + half * (want.abs() + tol))
+        assert not bool(bad[:n].any()), t.nonzero(bad[:n])[:4].tolist()
+        assert bool((y[n:] == 7).all()) and bool((y[3:n:41] == 0).all())
 
 
 def test_grouped_bf16_k_of_eights(t, B):
