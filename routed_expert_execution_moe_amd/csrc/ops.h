@@ -50,7 +50,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool glu, hipStream_t s);
 // its variants that stage tiles in LDS (product_tile.h), one source file per
 // pair of types
-enum class TileKind { kBig, kDeep, kShared };
+enum class TileKind { kBig, kHalf, kDeep, kShared };
 hipError_t launch_tile_bf16(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);
 hipError_t launch_tile_w4(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);
 hipError_t launch_tile_mx(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);

@@ -15,7 +15,8 @@ namespace moert {
 
 constexpr int kGroupWave = 256;     // pairs of one wave
 constexpr int kGroupOne = 4096;     // one workgroup of 16 waves
-constexpr int kGroupMany = 1024;    // chunk of a workgroup of 4 waves
+constexpr int kGroupFew = 1024;     // one workgroup of 4 waves
+constexpr int kGroupMany = 2048;    // chunk of a workgroup of 8 waves
 constexpr int kBuckets = kMaxExperts + 1;
 
 __device__ inline int group_bucket(const int32_t* ids, int64_t i, int64_t pairs, int E) {
@@ -53,8 +54,8 @@ __global__ __launch_bounds__(WAVES * 64) void pairs_rank_kernel(const int32_t* _
   int b[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) b[g] = group_bucket(ids, first + g * 64 + lane, pairs, E);
-  for (int i = tid; i < WAVES * kBuckets; i += T) (&s_next[0][0])[i] = 0;
-  __syncthreads();
+  for (int e = lane; e <= E; e += 64) s_next[wave][e] = 0;  // each wave its own
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
   for (int g = 0; g < G; ++g)
     if (b[g] >= 0) atomicAdd(&s_next[wave][b[g]], 1);
@@ -67,10 +68,16 @@ __global__ __launch_bounds__(WAVES * 64) void pairs_rank_kernel(const int32_t* _
     int total = 0, before = 0;
     if (e < E) {
       if (hist) {
-        for (int c = 0; c < n_chunks; ++c) {
-          const int n = hist[(int64_t)c * E + e];
-          total += n;
-          if (c < (int)blockIdx.x) before += n;
+        // sixteen chunks' counts requested before the first is added
+        for (int c0 = 0; c0 < n_chunks; c0 += 16) {
+          int n[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) n[i] = c0 + i < n_chunks ? hist[(int64_t)(c0 + i) * E + e] : 0;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            total += n[i];
+            before += c0 + i < (int)blockIdx.x ? n[i] : 0;
+          }
         }
       } else {
 #pragma unroll
@@ -136,13 +143,16 @@ size_t group_workspace(int64_t pairs, int E) {
 
 hipError_t launch_group_pairs(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* perm,
                               int32_t* ws, hipStream_t s) {
+  if (pairs <= kGroupFew)
+    return launch_op(pairs_rank_kernel<4>, dim3(1), dim3(256), s, ids, pairs, E, (const int32_t*)nullptr, 1,
+                     offsets, perm);
   if (pairs <= kGroupOne)
     return launch_op(pairs_rank_kernel<16>, dim3(1), dim3(1024), s, ids, pairs, E, (const int32_t*)nullptr, 1,
                      offsets, perm);
   const int chunks = (int)((pairs + kGroupMany - 1) / kGroupMany);
   hipError_t e = launch_op(pairs_hist_kernel, dim3(chunks), dim3(256), s, ids, pairs, E, ws);
   if (e != hipSuccess) return e;
-  return launch_op(pairs_rank_kernel<4>, dim3(chunks), dim3(256), s, ids, pairs, E, (const int32_t*)ws, chunks,
+  return launch_op(pairs_rank_kernel<8>, dim3(chunks), dim3(512), s, ids, pairs, E, (const int32_t*)ws, chunks,
                    offsets, perm);
 }
 

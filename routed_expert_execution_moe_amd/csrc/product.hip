@@ -205,33 +205,41 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
   return launch_small_as<AT, WT, GLU, 4, GLU ? 2 : 4>(a, s);
 }
 
-// Which variant, by the tiles that a call can make at most (us, MI355X, small /
-// Mid / Big; "up" is a GLU product of N = 1536, K = 2048 over 128 experts with 8
-// per token):
-//   Mid wants 64 tiles (129 with W4, whose small variant is the faster): W4A4
-//   4096x4096 at 64, 128 rows 11.8 / 12.6, 16.8 / 12.5; bf16 at 128, 256 rows
-//   29.5 / 32.1, 38.7 / 31.9; W4 at 128, 256, 512 rows 23.6 / 28, 30.2 / 28,
-//   57.8 / 28; up at 1 and 8 tokens W4A4 8.2 / 10.0, 17.3 / 13.5.
-//   Big wants 128 tiles of its own and, in the mean, 192 rows an expert: W4A4
-//   4096x4096 at 1,024 rows 19.4 Mid, 39.4 Big; at 4,096 rows 81 Mid, 45.8 Big; up
-//   at 1,024, 2,048 and 4,096 tokens 63 / 110, 98 / 114, 160 / 142.
-//   Mid is Shared beyond 256 tiles, one per CU: W4A4 2048x768 over 128 experts at
-//   256 tokens 34 Shared, 55 Deep; 128x4096x4096 (64 tiles) 14.5 Shared, 12.5 Deep.
+// Which variant, by the tiles that a call can make at most and by the mean rows
+// of an expert (us on MI355X; "up" is a GLU product of N = 1536, K = 2048 over 128
+// experts, "plain" one without GLU of N = 2048, K = 768, both with 8 experts a
+// token):
+//   Mid, not the small variant, from 64 tiles (W4, whose small variant is the
+//   faster: 129).  W4A4 4096x4096 at 64 and 128 rows 11.8 small, 12.6 Mid and
+//   16.8, 12.5; bf16 at 128 and 256 rows 29.5, 32.1 and 38.7, 31.9; W4 at 128, 512
+//   rows 23.6, 28 and 57.8, 29; W4A4 up at 1 and 8 tokens 8.2, 10.0 and 17.3, 13.5.
+//   Mid is Shared beyond 256 tiles, one per CU.  W4A4 plain at 256 tokens 34
+//   Shared, 55 Deep; 128x4096x4096 (64 tiles) 14.5 Shared, 12.5 Deep.
+//   Half from 257 tiles of its own and 96 rows.  W4A4 plain at 1,024, 2,048 and
+//   4,001 tokens (64, 128, 250 rows) 45 Half, 42 Mid and 58, 63 and 87, 106; bf16
+//   2048x4096x4096 72 Half, 112 Mid.
+//   Big from 256 (GLU 128) tiles of its own and: bf16 192 rows (GLU 128), W4A4 384
+//   (192), W4 768.  Plain at 4,001 and 8,192 tokens (250, 512 rows), Half and Big:
+//   bf16 212, 209 and 383, 310; W4A4 87, 126 and 213, 191; W4 132, 197 and 247, 293.
+//   Up at 2,048 and 4,096 tokens (128, 256 rows), Mid and Big: bf16 250, 222 and
+//   398, 293; W4A4 94, 97 and 152, 127; W4 136, 208 and 237, 275.
 template <int AT, int WT>
 static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
-  constexpr bool W4 = AT == MOE_BF16 && WT == MOE_MXFP4;
+  constexpr bool XM = AT == MOE_MXFP4, W4 = !XM && WT == MOE_MXFP4;
   // the tile kernels address the rows of x of a tile with 32-bit offsets and
   // read MXFP4 scales 16 at a time
   if (a.x_ld < (1 << 23) && (WT != MOE_MXFP4 || a.K >= 512)) {
-    const int64_t n_out = glu ? a.N / 2 : a.N;
-    const int64_t mid = op_max_tiles(a, 64) * ((n_out + 127) / 128);
-    const int64_t big = op_max_tiles(a, 256) * ((n_out + (glu ? 127 : 255)) / (glu ? 128 : 256));
+    const int64_t n_out = glu ? a.N / 2 : a.N, rows = a.n_rows / a.n_experts;
+    auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * ((n_out + n - 1) / n); };
     auto tile = [&](TileKind kind) {
-      if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, kind, s);
-      else if constexpr (WT == MOE_MXFP4) return launch_tile_w4(a, glu, kind, s);
+      if constexpr (XM) return launch_tile_mx(a, glu, kind, s);
+      else if constexpr (W4) return launch_tile_w4(a, glu, kind, s);
       else return launch_tile_bf16(a, glu, kind, s);
     };
-    if (big >= 128 && a.n_rows >= 192 * (int64_t)a.n_experts) return tile(TileKind::kBig);
+    const int64_t big = glu ? tiles(256, 128) : tiles(256, 256), mid = tiles(64, 128);
+    if (big >= (glu ? 128 : 256) && rows >= (W4 ? 768 : XM ? (glu ? 192 : 384) : glu ? 128 : 192))
+      return tile(TileKind::kBig);
+    if (!glu && tiles(128, 128) > 256 && rows >= 96) return tile(TileKind::kHalf);
     if (mid >= (W4 ? 129 : 64)) return tile(mid > 256 ? TileKind::kShared : TileKind::kDeep);
   }
   return glu ? launch_small<AT, WT, true>(a, s) : launch_small<AT, WT, false>(a, s);

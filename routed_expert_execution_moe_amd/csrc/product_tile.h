@@ -26,16 +26,20 @@
 // with the scaled converts right before its products.
 //
 // Shapes.  Big, 256 x 256 with two stages: (NI + 2) fragment reads per 2 NI
-// products, 0.63 at NI = 8, leave LDS bandwidth for the copies.  Mid, 64 x 128
-// (GLU 64 x 256), for products whose big tiles would leave CUs without one; there
-// a step's products last less than a memory latency, which Deep hides with more
-// stages and Shared with more workgroups on a CU (at most 80 KB of LDS each; the
-// GLU shapes with two operands at full width do not get there).
+// products, 0.63 at NI = 8, leave LDS bandwidth for the copies.  Half, 128 x 128,
+// and Mid, 64 x 128 (GLU 64 x 256), for products whose larger tiles would leave
+// CUs without one or spend their time before and after a short K.  They stay
+// within 80 KB of LDS, so that one workgroup's first and last latencies are
+// another's products; but Deep (Mid with more stages) has a CU to itself, where
+// there are too few tiles to share one, and so has every GLU tile but W4's.
 //
-// 4096 x 4096 x 4096 takes 45.8 us with MXFP4 operands (3.0 PFLOP/s; a step 1.9 us
-// against 0.85 us of products) and 113 us with bf16 (1.22 PFLOP/s; 1.25 at K =
-// 8192), bound by what the copies of all CUs together get: one tile alone on
-// the chip takes 1.5 and 1.15 us a step.
+// 4096 x 4096 x 4096 takes 44.0 us with MXFP4 operands (3.1 PFLOP/s) and 113 us
+// with bf16 (1.22 PFLOP/s; 1.25 at K = 8192).  Of 76,000 clocks of a W4A4 tile,
+// 33,000 are its products; 20,000 more go by in the 16 steps waiting for copies
+// and fragments, 16,000 while all CUs write their tiles at once, and 7,000 until
+// the first stage is there.  Steps of 64 bytes in four stages hide the waits of one
+// tile alone better (1.04 against 1.11 us per 128 bytes of bf16), but asking for
+// half cache lines costs more with all CUs at work (119 against 113 us).
 #pragma once
 
 #include <type_traits>
@@ -61,6 +65,13 @@ struct TileMid {
   static constexpr bool Unroll = false;
   static constexpr int Stages = WT == MOE_MXFP4 && AT == MOE_BF16 ? 3 : !Deep ? 2 : GLU ? 3 : 4;
   static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : 64;
+};
+
+template <int AT, int WT>
+struct TileHalf {
+  static constexpr int MaxI = 4, J = 1, Row = 128, Stages = 2;
+  static constexpr bool Unroll = false;
+  static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : 48;
 };
 
 template <int AT, int WT, class C>
@@ -542,6 +553,13 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
   if constexpr (C::MaxI == 2) {
     if (ni == 1) run(integral_constant<int, 1>{});
     else run(integral_constant<int, 2>{});
+  } else if constexpr (C::MaxI == 4) {
+    switch (ni) {
+      case 1: run(integral_constant<int, 1>{}); break;
+      case 2: run(integral_constant<int, 2>{}); break;
+      case 3: run(integral_constant<int, 3>{}); break;
+      default: run(integral_constant<int, 4>{}); break;
+    }
   } else {
     switch (ni) {
       case 1: run(integral_constant<int, 1>{}); break;
@@ -568,6 +586,7 @@ hipError_t launch_tile_as(const ProductArgs& a, hipStream_t s) {
 template <int AT, int WT>
 hipError_t launch_tile(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s) {
   constexpr bool W4 = AT == MOE_BF16 && WT == MOE_MXFP4;
+  if (kind == TileKind::kHalf && !glu) return launch_tile_as<AT, WT, false, TileHalf<AT, WT>>(a, s);
   if (kind == TileKind::kBig)
     return glu ? launch_tile_as<AT, WT, true, TileBig<AT, WT>>(a, s) : launch_tile_as<AT, WT, false, TileBig<AT, WT>>(a, s);
   // W4's stages are small enough for both at once; the other formats' GLU

@@ -195,9 +195,10 @@ def test_mx_gemm(t, B, M, N, K, act, out):
 
 
 GEMM_TILES = [  # enough tiles for each of the LDS variants; ends inside steps and scale chunks
-    (500, 1100, 544), (500, 1100, 1600), (129, 4100, 2080),           # 64 x 128 tiles, one per CU
-    (1500, 1500, 672), (1090, 2050, 2112),                           # 64 x 128 tiles, several per CU
-    (2050, 4100, 544), (2049, 4353, 1568), (2300, 4000, 4192),       # 256 x 256 tiles
+    (500, 1100, 544), (500, 1100, 1600), (129, 4100, 2080),      # 64 x 128 tiles, one per CU
+    (1500, 1500, 672), (1090, 2050, 2112),                      # 64 x 128 tiles, several per CU
+    (2050, 4100, 544), (2049, 4353, 1568), (2300, 4000, 4192),  # 128 x 128 tiles
+    (4100, 4097, 544), (4353, 3900, 1696), (3850, 4352, 4128),  # 256 x 256 tiles
 ]
 
 
