@@ -464,7 +464,7 @@ moe_status moe_mx_gemm(const void* x, moe_dtype x_dtype, const uint8_t* x_scales
  * receives the first position of each expert (offsets[E] = pairs with an
  * expert in 0..E-1), perm [T*k] the pair at each position, pairs of one expert
  * in ascending pair order; pairs whose id lies outside 0..E-1 (padding) take
- * the positions from offsets[E] on, as -1.  1 <= E <= 1024, T*k < 2^31 - 4096.
+ * the positions from offsets[E] on, as -1.  1 <= E <= 1024, T*k <= 2^24.
  * workspace (4-byte aligned) must hold moe_group_workspace(T, k, E) bytes (0
  * for up to 4,096 pairs, then it may be NULL) and belongs to the call until its
  * work has finished: calls that can overlap, captured graphs among them, need
@@ -484,8 +484,8 @@ moe_status moe_group_pairs(const int32_t* ids, int32_t T, int32_t k, int32_t E, 
  * = k the rows of x are tokens; with y_index = perm the rows of y are pairs.
  * offsets and the indices are read on the device and never on the host:
  * positions before offsets[0] or from offsets[E] on leave y as it was; an
- * x_index outside 0..n_x-1 (after the division; negative ones too) reads a row
- * of zeros; a y_index outside 0..n_y-1 writes nothing.  Offsets that do not
+ * x_index outside 0..n_x-1 (after the division; negative ones too) makes row(p)
+ * zeros; a y_index outside 0..n_y-1 writes nothing.  Offsets that do not
  * ascend within 0..n_rows leave the affected rows unspecified but read and
  * write nothing out of range.  If two positions name one row of y, which of
  * the two it holds is unspecified.
@@ -503,7 +503,7 @@ typedef struct {
   const void* x;             /* [n_x][K], ldx elements from row to row (MXFP4: K) */
   const uint8_t* x_scales;   /* MXFP4 x: [n_x][K/32], else NULL                   */
   int64_t ldx;
-  int32_t n_x;               /* rows of x; >= n_rows without x_index              */
+  int32_t n_x;               /* rows of x, >= 1; >= n_rows without x_index         */
   int32_t x_index_div;       /* >= 1                                              */
   const int32_t* x_index;    /* [n_rows] or NULL                                  */
   const void* w;
@@ -520,7 +520,7 @@ typedef struct {
 moe_status moe_grouped_gemm(const moe_grouped_args* args, moe_stream stream);
 
 /* y[t] = sum over ascending j of w[t][j] * p[t*k + j] in fp32, one rounding:
- * moe_merge's sum over rows that the caller holds.  p [T*k][H] (F32 or BF16,
+ * moe_merge's sum over rows that the caller holds.  p [T*k][H], H <= 2^30 (F32 or BF16,
  * ldp elements from row to row), w fp32 [T][k], y [T][H] (F32 or BF16, ldy).
  * ids [T][k] or NULL: pairs with an id outside 0..E-1 are left out (their rows
  * are not read), so a token without any expert gives a row of zeros.

@@ -9,6 +9,7 @@ namespace {
 constexpr int64_t kInt32Bytes = (int64_t)1 << 31;
 constexpr int64_t kMaxRows = kInt32Bytes - 4096;  // row counts, rounded up to tiles, stay int32
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int64_t kMaxPairs = (int64_t)1 << 24;  // each chunk of pairs sums the counts of all others
 
 int64_t elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 bool is_act(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
@@ -21,6 +22,7 @@ moe_status bad(const char* where, const char* why) {
 // a launch's status; HIP errors of calls without a context are not latched
 moe_status done(const char* where, hipError_t e) {
   if (e == hipSuccess) return MOE_OK;
+  (void)hipGetLastError();  // reported here, so not left for the thread's next caller
   if (e == hipErrorInvalidConfiguration)
     return bad(where, "too large: the call needs more workgroups than one launch may have");
   return hip_fail(nullptr, e, where);
@@ -87,6 +89,7 @@ static moe_status check_product(const char* me, const ProductArgs& a, int x_dtyp
   if (!aligned(a.x, 16) || !aligned(a.w, 16) || !aligned(a.y, elem_bytes(y_dtype)))
     return bad(me, "x and W must be 16-byte aligned and y aligned to its element");
   if ((int64_t)a.N * a.K / (wm ? 2 : 1) * (wm ? 1 : 2) >= kInt32Bytes) return bad(me, "a weight matrix must stay below 2^31 bytes");
+  if (a.n_x < 1) return bad(me, "x needs a row");  // positions without one read the first, for nothing
   if ((!a.x_index && a.n_x < a.n_rows) || (!a.y_index && a.n_y < a.n_rows))
     return bad(me, "x and y need a row for every position unless an index is given");
   if (a.x_index && a.n_x > 0 && (int64_t)(a.n_x - 1) * a.x_ld + a.x_ld >= kInt32Bytes)
@@ -160,7 +163,7 @@ extern "C" moe_status moe_grouped_gemm(const moe_grouped_args* g, moe_stream str
 
 // T*k pairs when the sizes are in range, else -1
 static int64_t pair_count(int32_t T, int32_t k, int32_t E) {
-  if (T < 0 || k < 1 || E < 1 || E > kMaxExperts || (int64_t)T * k >= kMaxRows) return -1;
+  if (T < 0 || k < 1 || E < 1 || E > kMaxExperts || (int64_t)T * k > kMaxPairs) return -1;
   return (int64_t)T * k;
 }
 
@@ -175,7 +178,7 @@ extern "C" moe_status moe_group_pairs(const int32_t* ids, int32_t T, int32_t k, 
   return guarded([&] {
     const char* me = "moe_group_pairs";
     const int64_t pairs = pair_count(T, k, E);
-    if (pairs < 0) return bad(me, "T must be >= 0, k >= 1, E in 1..1024 and T*k below 2^31 - 4096");
+    if (pairs < 0) return bad(me, "T must be >= 0, k >= 1, E in 1..1024 and T*k at most 2^24");
     if (!offsets || (pairs && (!ids || !perm))) return bad(me, "NULL argument");
     const size_t need = group_workspace(pairs, E);
     if (need && (!workspace || workspace_bytes < need)) return bad(me, "workspace smaller than moe_group_workspace()");
@@ -192,7 +195,7 @@ extern "C" moe_status moe_combine_pairs(const void* p, moe_dtype p_dtype, int64_
     const char* me = "moe_combine_pairs";
     if (!is_act(p_dtype) || !is_act(y_dtype))
       return fail(nullptr, MOE_EUNSUPPORTED, "moe_combine_pairs: p and y must be F32 or BF16");
-    if (T < 0 || k < 1 || H < 1) return bad(me, "T must be >= 0, k and H >= 1");
+    if (T < 0 || k < 1 || H < 1 || H > 1 << 30) return bad(me, "T must be >= 0, k >= 1 and H in 1..2^30");
     if (ids && E < 1) return bad(me, "E must be >= 1 with ids");
     if (T == 0) return MOE_OK;
     if (!p || !w || !y) return bad(me, "NULL argument");

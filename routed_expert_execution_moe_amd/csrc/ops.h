@@ -114,7 +114,9 @@ __device__ inline int op_scan(int v) {
 // l counts the tiles of its E/64 experts and a wave scan orders them; every
 // lane then gets the total, and find() the t-th tile: the lane that holds it,
 // then, its experts (at most 16) a lane each, the expert.  Offsets are clamped
-// into 0..n_rows, so bad ones cost results but no access out of range.
+// into 0..n_rows and the counts to what ascending ones can make (the launch
+// keeps that below 2^24, so no sum overflows): bad offsets cost results but
+// no access out of range.
 struct OpTiles {
   int incl, mine, total;
 
@@ -134,8 +136,10 @@ struct OpTiles {
       int lo;
       if (e < a.n_experts) mine += (range(a, e, &lo) + BM - 1) / BM;
     }
+    const int most = a.n_rows / BM + min(a.n_experts, a.n_rows);
+    mine = min(mine, most);
     incl = op_scan(mine);
-    total = __builtin_amdgcn_readlane(incl, 63);
+    total = min(__builtin_amdgcn_readlane(incl, 63), most);
   }
 
   __device__ inline bool find(const ProductArgs& a, int BM, int t, OpTile* out) const {

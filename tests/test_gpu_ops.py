@@ -461,6 +461,29 @@ def test_grouped_bad_indices_and_offsets(t, B, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("glu", [True, False])
+def test_grouped_overlapping_offsets(t, B, fmt, glu):
+    """Every expert claims all positions, in calls of each variant's size: many
+    more tiles than the launch has workgroups.  Rows are unspecified; nothing
+    outside the positions' rows is written."""
+    act, wt = fmt.split("-")
+    rng = np.random.default_rng(14)
+    for E, R, N, K in ((1024, 60, 34, 512), (300, 3000, 260, 512), (7, 3000, 4100, 512), (3, 2900, 5000, 512)):
+        log(f"grouped overlapping {fmt} E={E} R={R} N={N} glu={glu}")
+        x, w = Operand(t, rng, R, K, act), Experts(t, rng, 1, N, K, wt)
+        w.t = w.t.expand(E, -1, -1)
+        if w.scales is not None:
+            w.scales = w.scales.expand(E, -1, -1)
+        off = np.tile([0, R], E)[:E + 1]
+        y = _grouped(t, B, x, w, off, R, N, "bfloat16", n_y=R + 300, glu=glu)
+        assert bool((y[R:] == 7).all())
+        y = _grouped(t, B, x, w, [0] + [R] * E, R, N, "bfloat16", n_y=R + 300, glu=glu)  # all of it the first one's
+        want, size = OO.grouped_rows(x.v[:50], lambda e: w.v[0], [0, 50], 50, N, glu=glu)
+        _close(y[:50], want, _bound(size, want, K, glu), True, E)
+        assert bool((y[R:] == 7).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_grouped_rows_do_not_mix(t, B, fmt):
     """NaN weights of an expert without rows, and NaN rows of x outside the
     positions or of another expert, reach no other row."""

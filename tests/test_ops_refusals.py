@@ -116,6 +116,7 @@ def _grouped(**kw):
     (dict(offsets=A + 2), MOE_EINVAL),
     (dict(x_index=A + 1), MOE_EINVAL),
     (dict(n_x=7), MOE_EINVAL),
+    (dict(n_x=0, x_index=A), MOE_EINVAL),
     (dict(n_y=7), MOE_EINVAL),
     (dict(ldy=31), MOE_EINVAL),
     (dict(ldy=15, glu=1), MOE_EINVAL),
@@ -140,7 +141,7 @@ def test_group_refusals_and_workspace():
     assert B.moe_group_workspace(0, 8, 128) == 0
     big = B.moe_group_workspace(8192, 8, 256)
     assert 0 < big <= 4 * 256 * (8192 * 8 // 256)
-    for bad in ((-1, 8, 128), (8, 0, 128), (8, 8, 0), (8, 8, 1025), (1 << 28, 8, 4)):
+    for bad in ((-1, 8, 128), (8, 0, 128), (8, 8, 0), (8, 8, 1025), (1 << 28, 8, 4), ((1 << 24) + 1, 1, 4)):
         assert B.moe_group_workspace(*bad) == 0
         assert f(A, *bad, A, A, A, 1 << 40, None) == MOE_EINVAL
     assert f(None, 8, 8, 128, A, A, None, 0, None) == MOE_EINVAL
@@ -156,7 +157,7 @@ def test_group_refusals_and_workspace():
     (dict(p_dtype=MX), MOE_EUNSUPPORTED), (dict(y_dtype=9), MOE_EUNSUPPORTED), (dict(T=-1), MOE_EINVAL),
     (dict(k=0), MOE_EINVAL), (dict(H=0), MOE_EINVAL), (dict(ldp=63), MOE_EINVAL), (dict(ldy=63), MOE_EINVAL),
     (dict(ids=A, E=0), MOE_EINVAL), (dict(ids=A + 1), MOE_EINVAL), (dict(p=A + 2), MOE_EINVAL),
-    (dict(w=None), MOE_EINVAL), (dict(w=A + 2), MOE_EINVAL), (dict(T=0, p=None), 0),
+    (dict(H=(1 << 30) + 1, ldp=1 << 31, ldy=1 << 31), MOE_EINVAL), (dict(w=None), MOE_EINVAL), (dict(w=A + 2), MOE_EINVAL), (dict(T=0, p=None), 0),
 ])
 def test_combine_refusals(kw, status):
     a = dict(p=A, p_dtype=F32, ldp=64, w=A, ids=None, E=4, T=2, k=2, H=64, y=A, y_dtype=F32, ldy=64)
