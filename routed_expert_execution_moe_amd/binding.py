@@ -1,7 +1,8 @@
 """ctypes binding of libmoert.so: the C-ABI calls under the same names.
 
 Argument marshalling only: tensors become device pointers, torch streams
-become hipStream_t handles, statuses become exceptions.  Every step of the
+become hipStream_t handles, statuses become exceptions (the operators without
+a context also take sizes and strides from their tensors, and check them).  Every step of the
 MoE layer runs in the library's HIP kernels and host code.  torch is imported
 first so the library binds to the HIP runtime torch already loaded (both
 carry the SONAME libamdhip64.so.7): one runtime per process.
@@ -305,9 +306,13 @@ def moe_ctx_timing(ctx, reset=False) -> dict:
 # Sizes, dtypes and strides come from the tensors, so these also check what the
 # library cannot see: shapes that belong together, element types, contiguous
 # rows and one device.  The call is made with the tensors' device current, on
-# `stream` or on that device's current stream.
+# `stream` or on that device's current stream.  The checks are host time in
+# front of kernels of a few microseconds: contiguous tensors, the usual case,
+# pass _matrix and _whole in a few attribute reads, and only what does not is
+# looked at for the reason.
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _U8, _I32, _BF16, _F32 = (torch.uint8,), (torch.int32,), (torch.bfloat16,), (torch.float32,)
+_INT = 1 << 31
 
 
 def _need(ok, where, detail):
@@ -315,14 +320,8 @@ def _need(ok, where, detail):
         raise MoertError(MOE_EINVAL, where, detail)
 
 
-def _tensor(where, name, t, dims, dtypes, shape=None, contiguous=False):
-    """Checks one argument; `shape` entries of None are free.  A whole contiguous
-    tensor of the expected shape, the usual case, takes one line: these checks
-    are host time in front of kernels of a few microseconds."""
-    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_contiguous() and t.numel() < 1 << 31:
-        have = t.shape
-        if len(have) == dims and (shape is None or have == shape or shape[0] is None and have[-1] == shape[-1]):
-            return  # every shape given with free entries fixes the last one only
+def _check_tensor(where, name, t, dims, dtypes, shape=None, contiguous=False):
+    """Checks one argument; `shape` entries of None are free."""
     _need(isinstance(t, torch.Tensor), where, f"{name} must be a tensor")
     _need(t.dim() == dims, where, f"{name} must have {dims} dimensions, has {t.dim()}")
     _need(t.dtype in dtypes, where, f"{name}: dtype {t.dtype} is not one of {', '.join(map(str, dtypes))}")
@@ -334,12 +333,25 @@ def _tensor(where, name, t, dims, dtypes, shape=None, contiguous=False):
     else:
         _need(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1, where,
               f"{name}: the elements of a row must be contiguous")
-    _need(max(t.shape, default=0) < 1 << 31, where, f"{name} is too large")
+    _need(max(t.shape, default=0) < _INT, where, f"{name} is too large")
 
 
-def _ld(t):
-    """Elements from row to row of a matrix; a single row has no next one."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] + -t.shape[1] % 8
+def _matrix(where, name, t, dtypes):
+    """(rows, columns, elements from row to row) of a matrix with contiguous rows."""
+    if t.__class__ is torch.Tensor and t.dtype in dtypes and t.is_contiguous() and len(t.shape) == 2:
+        R, C = t.shape
+        if R < _INT and C < _INT:
+            return R, C, C
+    _check_tensor(where, name, t, 2, dtypes)
+    R, C = t.shape
+    return R, C, t.stride(0) if R > 1 else C + -C % 8  # a single row has no next one
+
+
+def _whole(where, name, t, dtypes, shape):
+    """Checks a contiguous argument of this shape."""
+    if t.__class__ is torch.Tensor and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return
+    _check_tensor(where, name, t, len(shape), dtypes, shape, True)
 
 
 def _call(where, fn, tensors, stream, *args):
@@ -349,12 +361,11 @@ def _call(where, fn, tensors, stream, *args):
         if t is not None and (t.get_device() != dev or dev < 0):
             _need(t.is_cuda, where, f"tensors must be on the GPU, not on {t.device}")
             _need(False, where, "tensors are on different devices")
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None and not isinstance(stream, int):
         _need(stream.device.index == dev, where, f"stream of {stream.device}, tensors on cuda:{dev}")
+        stream = stream.cuda_stream
     if dev == torch._C._cuda_getDevice():
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(dev)
-        status = fn(*args, stream if isinstance(stream, int) else stream.cuda_stream)
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream)
     else:
         with torch.cuda.device(dev):
             status = fn(*args, _stream(stream))
@@ -365,52 +376,52 @@ def _call(where, fn, tensors, stream, *args):
 def moe_mx_quantize(x, codes, scales, stream=None):
     """x [R, C] f32 or bf16 (rows may be strided) -> codes uint8 [R, C/2], scales uint8 [R, C/32]."""
     me = "moe_mx_quantize"
-    _tensor(me, "x", x, 2, _FLOATS)
-    R, C = x.shape
+    R, C, ld = _matrix(me, "x", x, _FLOATS)
     _need(C % 32 == 0, me, "the columns must be a multiple of 32")
-    _tensor(me, "codes", codes, 2, _U8, (R, C // 2), True)
-    _tensor(me, "scales", scales, 2, _U8, (R, C // 32), True)
-    _call(me, lib().moe_mx_quantize, (x, codes, scales), stream, _ptr(x), _FLOATS[x.dtype], R, C, _ld(x),
-          _ptr(codes), _ptr(scales))
+    _whole(me, "codes", codes, _U8, (R, C // 2))
+    _whole(me, "scales", scales, _U8, (R, C // 32))
+    _call(me, lib().moe_mx_quantize, (x, codes, scales), stream, x.data_ptr(), _FLOATS[x.dtype], R, C, ld,
+          codes.data_ptr(), scales.data_ptr())
 
 
 def moe_mx_dequantize(codes, scales, y, stream=None):
     """codes uint8 [R, C/2], scales uint8 [R, C/32] -> y [R, C] f32 or bf16 (rows may be strided)."""
     me = "moe_mx_dequantize"
-    _tensor(me, "y", y, 2, _FLOATS)
-    R, C = y.shape
+    R, C, ld = _matrix(me, "y", y, _FLOATS)
     _need(C % 32 == 0, me, "the columns must be a multiple of 32")
-    _tensor(me, "codes", codes, 2, _U8, (R, C // 2), True)
-    _tensor(me, "scales", scales, 2, _U8, (R, C // 32), True)
-    _call(me, lib().moe_mx_dequantize, (y, codes, scales), stream, _ptr(codes), _ptr(scales), R, C, _ptr(y),
-          _FLOATS[y.dtype], _ld(y))
+    _whole(me, "codes", codes, _U8, (R, C // 2))
+    _whole(me, "scales", scales, _U8, (R, C // 32))
+    _call(me, lib().moe_mx_dequantize, (y, codes, scales), stream, codes.data_ptr(), scales.data_ptr(), R, C,
+          y.data_ptr(), _FLOATS[y.dtype], ld)
 
 
 def _rows_operand(me, x, x_scales):
-    """(K, dtype, ldx) of x: bf16 rows, or codes with their scales."""
+    """(rows, K, dtype, ldx) of x: bf16 rows, or codes with their scales."""
     if x_scales is None:
-        _tensor(me, "x", x, 2, _BF16)
-        return x.shape[1], MOE_BF16, _ld(x)
-    _tensor(me, "x", x, 2, _U8, contiguous=True)
-    K = x.shape[1] * 2
-    _need(K % 32 == 0, me, "K must be a multiple of 32")
-    _tensor(me, "x_scales", x_scales, 2, _U8, (x.shape[0], K // 32), True)
-    return K, MOE_MXFP4, K
+        R, K, ld = _matrix(me, "x", x, _BF16)
+        return R, K, MOE_BF16, ld
+    R, C, ld = _matrix(me, "x", x, _U8)
+    _need(R < 2 or ld == C, me, "x: codes must be contiguous")
+    _need(C % 16 == 0, me, "K must be a multiple of 32")
+    _whole(me, "x_scales", x_scales, _U8, (R, C // 16))
+    return R, 2 * C, MOE_MXFP4, 2 * C
 
 
 def moe_mx_gemm(x, w_codes, w_scales, y, x_scales=None, stream=None):
     """y [M, N] (f32 or bf16) = x W^T, W as codes uint8 [N, K/2] and scales uint8
     [N, K/32]; x bf16 [M, K], or codes uint8 [M, K/2] with x_scales [M, K/32]."""
     me = "moe_mx_gemm"
-    K, x_dtype, ldx = _rows_operand(me, x, x_scales)
+    M, K, x_dtype, ldx = _rows_operand(me, x, x_scales)
     _need(K % 32 == 0, me, "K must be a multiple of 32")
-    _tensor(me, "w_codes", w_codes, 2, _U8, (None, K // 2), True)
-    N = w_codes.shape[0]
-    _tensor(me, "w_scales", w_scales, 2, _U8, (N, K // 32), True)
-    _tensor(me, "y", y, 2, _FLOATS, (x.shape[0], N))
-    _call(me, lib().moe_mx_gemm, (x, x_scales, w_codes, w_scales, y), stream, _ptr(x), x_dtype,
-          _ptr(x_scales), ldx, _ptr(w_codes), _ptr(w_scales), _ptr(y), _FLOATS[y.dtype], _ld(y), x.shape[0],
-          N, K)
+    N, C, _ = _matrix(me, "w_codes", w_codes, _U8)
+    _whole(me, "w_codes", w_codes, _U8, (N, K // 2))
+    _whole(me, "w_scales", w_scales, _U8, (N, K // 32))
+    Y, C, ldy = _matrix(me, "y", y, _FLOATS)
+    if Y != M or C != N:
+        _need(False, me, f"y: shape {(Y, C)}, expected {(M, N)}")
+    _call(me, lib().moe_mx_gemm, (x, x_scales, w_codes, w_scales, y), stream, x.data_ptr(), x_dtype,
+          _ptr(x_scales), ldx, w_codes.data_ptr(), w_scales.data_ptr(), y.data_ptr(), _FLOATS[y.dtype], ldy, M, N,
+          K)
 
 
 def moe_group_workspace(T, k, E):
@@ -421,16 +432,16 @@ def moe_group_pairs(ids, n_experts, offsets, perm, workspace=None, stream=None):
     """ids int32 [T, k] -> offsets int32 [E+1], perm int32 [T*k]; workspace: any
     contiguous tensor of at least moe_group_workspace(T, k, E) bytes."""
     me = "moe_group_pairs"
-    _tensor(me, "ids", ids, 2, _I32, contiguous=True)
-    T, k = ids.shape
-    _tensor(me, "offsets", offsets, 1, _I32, (n_experts + 1,), True)
-    _tensor(me, "perm", perm, 1, _I32, (T * k,), True)
+    T, k, ld = _matrix(me, "ids", ids, _I32)
+    _need(T < 2 or ld == k, me, "ids must be contiguous")
+    _whole(me, "offsets", offsets, _I32, (n_experts + 1,))
+    _whole(me, "perm", perm, _I32, (T * k,))
     nbytes = 0
     if workspace is not None:
-        _need(workspace.is_contiguous(), me, "workspace must be contiguous")
+        _need(isinstance(workspace, torch.Tensor) and workspace.is_contiguous(), me, "workspace must be a contiguous tensor")
         nbytes = workspace.numel() * workspace.element_size()
-    _call(me, lib().moe_group_pairs, (ids, offsets, perm, workspace), stream, _ptr(ids), T, k, n_experts,
-          _ptr(offsets), _ptr(perm), _ptr(workspace), nbytes)
+    _call(me, lib().moe_group_pairs, (ids, offsets, perm, workspace), stream, ids.data_ptr(), T, k, n_experts,
+          offsets.data_ptr(), perm.data_ptr(), _ptr(workspace), nbytes)
 
 
 def moe_grouped_gemm(x, w, offsets, y, x_scales=None, w_scales=None, x_index=None, x_index_div=1,
@@ -441,29 +452,38 @@ def moe_grouped_gemm(x, w, offsets, y, x_scales=None, w_scales=None, x_index=Non
     y [n_y, N], or [n_y, N/2] with glu; x_index, y_index int32 [n_rows].  The
     positions are those of an index, else the rows of x."""
     me = "moe_grouped_gemm"
-    K, x_dtype, ldx = _rows_operand(me, x, x_scales)
-    if w_scales is None:
-        _tensor(me, "w", w, 3, _BF16, (None, None, K))
-        w_dtype, row = MOE_BF16, K
-    else:
-        _tensor(me, "w", w, 3, _U8, (None, None, K // 2))
-        _tensor(me, "w_scales", w_scales, 3, _U8, (w.shape[0], w.shape[1], K // 32))
-        _need(w.shape[1] == 1 or w_scales.stride(1) == K // 32, me, "w_scales: rows of one expert must be contiguous")
-        w_dtype, row = MOE_MXFP4, K // 2
+    n_x, K, x_dtype, ldx = _rows_operand(me, x, x_scales)
+    row, dtypes = (K, _BF16) if w_scales is None else (K // 2, _U8)
+    if not (w.__class__ is torch.Tensor and w.is_contiguous() and w.dtype in dtypes and len(w.shape) == 3
+            and w.shape[2] == row and max(w.shape) < _INT):
+        _check_tensor(me, "w", w, 3, dtypes, (None, None, row))
+        _need(w.shape[1] == 1 or w.stride(1) == row, me, "w: rows of one expert must be contiguous")
     E, N = w.shape[:2]
-    _need(N == 1 or w.stride(1) == row, me, "w: rows of one expert must be contiguous")
-    _tensor(me, "offsets", offsets, 1, _I32, (E + 1,), True)
-    index = x_index if x_index is not None else y_index
-    n_rows = x.shape[0] if index is None else index.shape[0]
-    for name, t in (("x_index", x_index), ("y_index", y_index)):
-        if t is not None:
-            _tensor(me, name, t, 1, _I32, (n_rows,), True)
-    _tensor(me, "y", y, 2, _FLOATS, (None, N // 2 if glu else N))
-    size = w.element_size()
-    a = GroupedArgs(E, n_rows, N, K, x_dtype, w_dtype, _FLOATS[y.dtype], 1 if glu else 0, _ptr(x),
-                    _ptr(x_scales), ldx, x.shape[0], x_index_div, _ptr(x_index), _ptr(w), _ptr(w_scales),
-                    w.stride(0) * size if E > 1 else 0, w_scales.stride(0) if w_scales is not None and E > 1 else 0,
-                    _ptr(offsets), _ptr(y), _ld(y), y.shape[0], 0, _ptr(y_index))
+    ws_ptr, ws_stride = None, 0
+    if w_scales is not None:
+        _need(K % 32 == 0, me, "K must be a multiple of 32")
+        if not (w_scales.__class__ is torch.Tensor and w_scales.is_contiguous() and w_scales.dtype in _U8
+                and w_scales.shape == (E, N, K // 32)):
+            _check_tensor(me, "w_scales", w_scales, 3, _U8, (E, N, K // 32))
+            _need(N == 1 or w_scales.stride(1) == K // 32, me, "w_scales: rows of one expert must be contiguous")
+        ws_ptr = w_scales.data_ptr()
+        ws_stride = w_scales.stride(0) if E > 1 else 0
+    _whole(me, "offsets", offsets, _I32, (E + 1,))
+    n_rows = n_x
+    if x_index is not None or y_index is not None:
+        index = y_index if x_index is None else x_index
+        _check_tensor(me, "x_index" if index is x_index else "y_index", index, 1, _I32, None, True)
+        n_rows = index.shape[0]
+        if y_index is not None and y_index is not index:
+            _whole(me, "y_index", y_index, _I32, (n_rows,))
+    _need(0 < x_index_div < _INT, me, "x_index_div must be >= 1")
+    n_y, cols, ldy = _matrix(me, "y", y, _FLOATS)
+    if cols != (N // 2 if glu else N):
+        _need(False, me, f"y has {cols} columns, expected {N // 2 if glu else N}")
+    a = GroupedArgs(E, n_rows, N, K, x_dtype, MOE_BF16 if w_scales is None else MOE_MXFP4, _FLOATS[y.dtype],
+                    1 if glu else 0, x.data_ptr(), _ptr(x_scales), ldx, n_x, x_index_div, _ptr(x_index),
+                    w.data_ptr(), ws_ptr, w.stride(0) * w.element_size() if E > 1 else 0, ws_stride,
+                    offsets.data_ptr(), y.data_ptr(), ldy, n_y, 0, _ptr(y_index))
     _call(me, lib().moe_grouped_gemm, (x, x_scales, w, w_scales, offsets, y, x_index, y_index), stream,
           ctypes.byref(a))
 
@@ -472,16 +492,19 @@ def moe_combine_pairs(p, w, y, ids=None, n_experts=0, stream=None):
     """y [T, H] = sum over j of w[t, j] * p[t*k + j]; p [T*k, H], w f32 [T, k];
     with ids int32 [T, k], pairs outside 0..n_experts-1 are left out."""
     me = "moe_combine_pairs"
-    _tensor(me, "w", w, 2, _F32, contiguous=True)
-    T, k = w.shape
-    _tensor(me, "p", p, 2, _FLOATS)
-    _need(p.shape[0] == T * k, me, f"p: {p.shape[0]} rows, expected {T * k}")
-    H = p.shape[1]
-    _tensor(me, "y", y, 2, _FLOATS, (T, H))
+    T, k, ld = _matrix(me, "w", w, _F32)
+    _need(T < 2 or ld == k, me, "w must be contiguous")
+    R, H, ldp = _matrix(me, "p", p, _FLOATS)
+    Y, C, ldy = _matrix(me, "y", y, _FLOATS)
+    if R != T * k or Y != T or C != H:
+        _need(False, me, f"w {(T, k)}, p {(R, H)} and y {(Y, C)} do not belong together")
     if ids is not None:
-        _tensor(me, "ids", ids, 2, _I32, (T, k), True)
-    _call(me, lib().moe_combine_pairs, (p, w, y, ids), stream, _ptr(p), _FLOATS[p.dtype], _ld(p), _ptr(w),
-          _ptr(ids), n_experts, T, k, H, _ptr(y), _FLOATS[y.dtype], _ld(y))
+        _whole(me, "ids", ids, _I32, (T, k))
+        _need(0 < n_experts < _INT, me, "ids need n_experts >= 1")
+    else:
+        n_experts = 0
+    _call(me, lib().moe_combine_pairs, (p, w, y, ids), stream, p.data_ptr(), _FLOATS[p.dtype], ldp, w.data_ptr(),
+          _ptr(ids), n_experts, T, k, H, y.data_ptr(), _FLOATS[y.dtype], ldy)
 
 
 def moe_strerror(status: int) -> str:

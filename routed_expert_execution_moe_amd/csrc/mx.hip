@@ -9,24 +9,34 @@
 // to -127 anyway).  The division by the block's power of two, the rounding to
 // the e2m1 grid with ties to even and the saturation at 6 are the gfx950
 // scaled convert; the sign of what rounded to zero is taken off afterwards.
+//
+// HBM bounds both ways: 32768 x 4096 fp32 to MXFP4 104 us (5.8 TB/s), back 117 us
+// (5.2 TB/s; a plain copy reaches 5.1).  Four rows a thread at once were slower (130
+// us), and so were stores past the caches (back: 211 us).
 #include "ops.h"
 
 namespace moert {
 
 constexpr int kMxThreads = 256;
 
+template <bool Stream, typename V>
+__device__ inline V mx_load(const uint8_t* p) {
+  if constexpr (Stream) return __builtin_nontemporal_load((const V*)p);
+  else return *(const V*)p;
+}
+
 // 8 elements of the row piece at x, as fp32
-template <bool F32>
+template <bool F32, bool Stream>
 __device__ inline void mx_load8(const uint8_t* x, float (&v)[8]) {
   if constexpr (F32) {
-    const op_f32x4 a = *(const op_f32x4*)x, b = *(const op_f32x4*)(x + 16);
+    const op_f32x4 a = mx_load<Stream, op_f32x4>(x), b = mx_load<Stream, op_f32x4>(x + 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[i] = a[i];
       v[4 + i] = b[i];
     }
   } else {
-    const op_u32x4 a = *(const op_u32x4*)x;
+    const op_u32x4 a = mx_load<Stream, op_u32x4>(x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(a[i] << 16);
@@ -60,7 +70,7 @@ __device__ inline uint32_t mx_encode8(const float (&v)[8], uint32_t* scale) {
 }
 
 // One row per blockIdx.y step, 8 elements per thread.
-template <bool F32>
+template <bool F32, bool Stream>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const uint8_t* __restrict__ x, int64_t rows,
                                                                 int cols, int64_t ld_bytes,
                                                                 uint8_t* __restrict__ codes,
@@ -70,7 +80,7 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const uint8_t* 
   if (c >= n) return;  // whole blocks of four lanes leave together: n is a multiple of 4
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     float v[8];
-    mx_load8<F32>(x + r * ld_bytes + (int64_t)c * (F32 ? 32 : 16), v);
+    mx_load8<F32, Stream>(x + r * ld_bytes + (int64_t)c * (F32 ? 32 : 16), v);
     uint32_t s;
     const uint32_t q = mx_encode8(v, &s);
     *(uint32_t*)(codes + r * (cols >> 1) + (int64_t)c * 4) = q;
@@ -123,8 +133,15 @@ static dim3 mx_grid(int64_t rows, int cols) {
 
 hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int cols, int64_t ldx, uint8_t* codes,
                               uint8_t* scales, hipStream_t s) {
-  return launch_op(f32 ? mx_quantize_kernel<true> : mx_quantize_kernel<false>, mx_grid(rows, cols),
-                   dim3(kMxThreads), s, (const uint8_t*)x, rows, cols, ldx * (f32 ? 4 : 2), codes, scales);
+  // An x that the memory-side cache cannot hold next to the codes is read past
+  // the caches, which then keep the codes for their reader: 32768 x 4096 fp32 and
+  // back 249 -> 215 us (the quantiser alone 104 -> 109).  Smaller ones may still lie
+  // there from their writer: 8192 x 4096 bf16 16 us, 18 past the caches.
+  const bool stream = rows * cols * (f32 ? 4 : 2) >= (int64_t)128 << 20;
+  auto k = f32 ? (stream ? mx_quantize_kernel<true, true> : mx_quantize_kernel<true, false>)
+               : (stream ? mx_quantize_kernel<false, true> : mx_quantize_kernel<false, false>);
+  return launch_op(k, mx_grid(rows, cols), dim3(kMxThreads), s, (const uint8_t*)x, rows, cols,
+                   ldx * (f32 ? 4 : 2), codes, scales);
 }
 
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,

@@ -8,7 +8,9 @@
 // so ranks follow the pair order and no atomic decides anything.  Up to
 // kGroupOne pairs are one workgroup's work.  Beyond that a first launch writes
 // each chunk's histogram to the workspace and the second sums, per expert, the
-// histograms before its own chunk and all of them.
+// histograms before its own chunk and all of them, sixteen loads in flight (one
+// after the other they took 15 of 22 us at 65,536 pairs and 256 experts).
+// Latency bounds it: 3.4 us for 64 pairs, 7 for 4,096, 3.3 + 7.2 for 65,536.
 #include "ops.h"
 
 namespace moert {
@@ -159,7 +161,8 @@ hipError_t launch_group_pairs(const int32_t* ids, int64_t pairs, int E, int32_t*
 // ------------------------------------------------------------------ combine
 // y[t][h] = sum over ascending j of w[t][j] * p[t*k + j][h].  A thread holds V
 // columns of one token; eight rows are requested before the first product, so
-// their latencies overlap.
+// their latencies overlap.  HBM bounds it: 65,536 fp32 rows of 4,096 into 8,192
+// bf16 rows take 197 us, 5.8 TB/s (a plain copy reaches 5.1); eight tokens 3.5 us.
 template <bool PF32, bool YF32, int V>
 __global__ __launch_bounds__(256) void combine_kernel(const uint8_t* __restrict__ p, int64_t ldp,
                                                       const float* __restrict__ w,

@@ -17,6 +17,12 @@
 //   bf16 x MXFP4    slice s, lane group g: k = 32g + 8s + [0,8): a lane's codes
 //                   are one 16-byte piece under one scale
 //   MXFP4 x MXFP4   lane group g: k = 32g + [0,32), the scaled MFMA's own order
+//
+// One token against 4096 x 4096 in MXFP4 (8.9 MB) takes 5.8 us of kernel and
+// eight tokens of the same 7.7, five and six of them launch, first loads and the
+// waves' sums; 64 x 4096 x 4096 takes 15.3 us in 32 x 32 blocks.  What bounds it
+// past a few rows is its loads: fragments come through the vector cache once
+// per wave, (MI + NB) of them per MI*NB products.
 #include <type_traits>
 
 #include "ops.h"

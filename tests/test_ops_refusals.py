@@ -205,12 +205,15 @@ def test_binding_refusals():
     _refused(B.moe_grouped_gemm, x, we, off, yg, x_index=perm, y_index=perm[:7])
     _refused(B.moe_grouped_gemm, x, we[:, ::2], off, yg[:, :3], x_index=perm)
     _refused(B.moe_grouped_gemm, x, we[..., :32], off, yg, x_index=perm)
+    _refused(B.moe_grouped_gemm, x, we, off, yg, x_index=perm, x_index_div=(1 << 32) + 2)
+    _refused(B.moe_grouped_gemm, x, we, off, yg, x_index=perm.long())
     p, cw, cy = torch.zeros(8, 6), torch.zeros(4, 2), torch.zeros(4, 6)
     assert "GPU" in _refused(B.moe_combine_pairs, p, cw, cy)
     _refused(B.moe_combine_pairs, p[:7], cw, cy)
     _refused(B.moe_combine_pairs, p, cw.double(), cy)
     _refused(B.moe_combine_pairs, p, cw, cy[:, :5])
     _refused(B.moe_combine_pairs, p, cw, cy, ids=ids[:3])
+    _refused(B.moe_combine_pairs, p, cw, cy, ids=ids, n_experts=1 << 32)
 
 
 def test_oracle_quantiser():
