@@ -1,12 +1,13 @@
 // Products y = x W^T, dense or ragged by expert: the variants that stage tiles
 // of both operands in LDS.
 //
-// A workgroup of four waves owns a tile of up to 32*MaxI rows of x against
-// 128*J rows of W (with GLU, J = 2: 128 gate rows and the matching 128 up rows),
-// in v_mfma 32x32 blocks with fp32 accumulation.  The waves stand side by
-// side: each takes all of the tile's rows by 32*J rows of W, NI x J blocks with
-// NI = ceil(rows / 32), so a short last tile of an expert costs only the blocks
-// it fills and loads every wave alike.
+// A workgroup owns a tile of up to 32 MaxI WavesM rows of x against 128 J rows of
+// W (with GLU, J = 2: 128 gate rows and the matching 128 up rows), in v_mfma 32x32
+// blocks with fp32 accumulation.  Four waves stand side by side along W, 32 J rows
+// each, against all row blocks of the tile, NI = ceil(rows / 32) of them; eight
+// waves stand in two such rows, which take the row blocks in turn.  So a short
+// last tile of an expert costs only the blocks it fills and loads every wave
+// alike.
 //
 // K goes in steps of 128 or 64 bytes of a row (64 bf16 or 256 MXFP4 in 128)
 // through a ring of LDS stages that direct-to-LDS loads fill Stages - 1 steps ahead; 16-byte
@@ -25,21 +26,24 @@
 // 32-element piece; bf16 x MXFP4 keeps W as codes in LDS and expands a fragment
 // with the scaled converts right before its products.
 //
-// Shapes.  Big, 256 x 256 with two stages: (NI + 2) fragment reads per 2 NI
-// products, 0.63 at NI = 8, leave LDS bandwidth for the copies.  Half, 128 x 128,
-// and Mid, 64 x 128 (GLU 64 x 256), for products whose larger tiles would leave
-// CUs without one or spend their time before and after a short K.  They stay
-// within 80 KB of LDS, so that one workgroup's first and last latencies are
-// another's products; but Deep (Mid with more stages) has a CU to itself, where
-// there are too few tiles to share one, and so has every GLU tile but W4's.
+// Shapes.  Big, 256 x 256 with eight waves and two stages: a wave reads (NI + 2)
+// fragments from LDS per 2 NI products, 0.75 at NI = 4, and two waves on a SIMD fill
+// each other's waits (four waves with 128 x 2 blocks read 0.63 and leave one wave
+// alone with its own: W4A4 8192 x 4096 x 4096 86.4 us, eight 80.0; bf16 222 and 215).
+// Half, 128 x 128, and Mid, 64 x 128 (GLU 64 x 256), with four waves, for products
+// whose larger tiles would leave CUs without one or spend their time before and
+// after a short K.  They stay within 80 KB of LDS, so that one workgroup's first
+// and last latencies are another's products; but Deep (Mid with more stages) has a
+// CU to itself, where there are too few tiles to share one, and so has every GLU
+// tile but W4's.
 //
-// 4096 x 4096 x 4096 takes 44.0 us with MXFP4 operands (3.1 PFLOP/s) and 113 us
-// with bf16 (1.22 PFLOP/s; 1.25 at K = 8192).  Of 76,000 clocks of a W4A4 tile,
-// 33,000 are its products; 20,000 more go by in the 16 steps waiting for copies
-// and fragments, 16,000 while all CUs write their tiles at once, and 7,000 until
-// the first stage is there.  Steps of 64 bytes in four stages hide the waits of one
-// tile alone better (1.04 against 1.11 us per 128 bytes of bf16), but asking for
-// half cache lines costs more with all CUs at work (119 against 113 us).
+// 8192 x 4096 x 4096 takes 80 us with MXFP4 operands (3.4 PFLOP/s) and 215 us with
+// bf16 (1.28).  A Big tile's time in clocks, four waves, 4096 x 4096 x 4096, W4A4:
+// 33,000 of products within a loop of 53,000, whose rest waits for copies and
+// fragments; 20,000 while all CUs write their tiles at once; 7,600 until the first
+// stage is there.  Steps of 64 bytes in four stages hide the waits of one tile
+// alone better (1.04 against 1.11 us per 128 bytes of bf16), but asking for half
+// cache lines costs more with all CUs at work (119 against 113 us).
 #pragma once
 
 #include <type_traits>
@@ -48,20 +52,19 @@
 
 namespace moert {
 
-constexpr int kTlThreads = 256;
 
 typedef unsigned int tile_bytes16 __attribute__((ext_vector_type(4), aligned(1)));
 
 template <int AT, int WT>
 struct TileBig {
   static constexpr bool W4 = WT == MOE_MXFP4 && AT == MOE_BF16;
-  static constexpr int MaxI = 8, J = 2, Row = 128, Stages = W4 ? 3 : 2;
+  static constexpr int Waves = 8, MaxI = 4, J = 2, Row = 128, Stages = W4 ? 3 : 2;
   static constexpr bool Unroll = !W4;
-  static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : W4 ? 64 : 48;
+  static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : W4 ? 64 : 32;  // 48: registers spill, 82.4 us for 80.0
 };
 template <int AT, int WT, bool GLU, bool Deep>
 struct TileMid {
-  static constexpr int MaxI = 2, J = GLU ? 2 : 1, Row = 128;
+  static constexpr int Waves = 4, MaxI = 2, J = GLU ? 2 : 1, Row = 128;
   static constexpr bool Unroll = false;
   static constexpr int Stages = WT == MOE_MXFP4 && AT == MOE_BF16 ? 3 : !Deep ? 2 : GLU ? 3 : 4;
   static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : 64;
@@ -69,7 +72,7 @@ struct TileMid {
 
 template <int AT, int WT>
 struct TileHalf {
-  static constexpr int MaxI = 4, J = 1, Row = 128, Stages = 2;
+  static constexpr int Waves = 4, MaxI = 4, J = 1, Row = 128, Stages = 2;
   static constexpr bool Unroll = false;
   static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : 48;
 };
@@ -77,16 +80,17 @@ struct TileHalf {
 template <int AT, int WT, class C>
 struct TileShape {
   static constexpr bool XM = AT == MOE_MXFP4, WM = WT == MOE_MXFP4, W4 = WM && !XM;
-  static constexpr int M = 32 * C::MaxI, N = 128 * C::J;
+  static constexpr int Waves = C::Waves, WavesM = Waves / 4, Threads = Waves * 64;
+  static constexpr int M = 32 * C::MaxI * WavesM, N = 128 * C::J;
   static constexpr int Row = C::Row, Slices = Row / 32, Parts = Row / 16;  // bytes, slices, 16-byte pieces of a row per step
   static constexpr int WRow = W4 ? Row / 4 : Row;                         // bytes of a W row per step
   static_assert(!W4 || Row == 128, "a W4 row's step is two pieces");
   static constexpr int StageA = M * Row, StageB = N * WRow, Stage = StageA + StageB;
   static constexpr int CopyRows = 1024 / Row;   // rows of one copy of a wave
-  static constexpr int BLoads = StageB / 4096;  // per wave and step
+  static constexpr int BLoads = StageB / (Waves * 1024);  // per wave and step
   static constexpr int ScalePitch = C::ScaleBytes + 8;  // 2 banks more than a multiple of 4
   static constexpr int ScaleRows = XM ? M + N : WM ? N : 0;
-  static constexpr int ScaleTurns = (ScaleRows + kTlThreads - 1) / kTlThreads;
+  static constexpr int ScaleTurns = (ScaleRows + Threads - 1) / Threads;
   static constexpr int StepBlocks = XM ? Row / 16 : 2;   // scales of a row per step
   static constexpr int ChunkSteps = WM ? C::ScaleBytes / StepBlocks : 1;
 };
@@ -114,7 +118,7 @@ __device__ inline void tile_sync() {
 }
 
 template <int AT, int WT, bool GLU, class C>
-__global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs a) {
+__global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductArgs a) {
   using S = TileShape<AT, WT, C>;
   using std::integral_constant;
   constexpr int J = C::J, Stages = C::Stages;
@@ -146,6 +150,7 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;  // the wave's place along the rows of x and of W
   const int lr = lane & 31, kg = lane >> 5;
   const int K = a.K, blocks = K / 32;
   const int x_bytes = S::XM ? K / 2 : K * 2;
@@ -175,7 +180,7 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
 
   auto run = [&](auto ni_c) {
     constexpr int NI = decltype(ni_c)::value;
-    constexpr int ALoads = (NI * 32 + 4 * S::CopyRows - 1) / (4 * S::CopyRows);
+    constexpr int ALoads = (NI * S::WavesM * 32 + S::Waves * S::CopyRows - 1) / (S::Waves * S::CopyRows);
     constexpr int Group = ALoads + S::BLoads;  // copies of one wave per step
 
     // Copies.  A lane's piece is the same in every row it copies: 4 CopyRows rows
@@ -185,18 +190,18 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     uint32_t a_off[ALoads], b_off[S::BLoads];
 #pragma unroll
     for (int q = 0; q < ALoads; ++q)
-      a_off[q] = (uint32_t)x_row((q * 4 + wave) * S::CopyRows + cr) * (uint32_t)a.x_ld + piece * 16;
+      a_off[q] = (uint32_t)x_row((q * S::Waves + wave) * S::CopyRows + cr) * (uint32_t)a.x_ld + piece * 16;
     const int half = (lane & 1) ^ ((lane >> 4) & 1);  // W4: rows 8 apart share banks, their halves swap
 #pragma unroll
     for (int q = 0; q < S::BLoads; ++q)
-      b_off[q] = S::W4 ? (uint32_t)w_row((q * 4 + wave) * 32 + (lane >> 1)) * (uint32_t)(K / 2) + half * 16
-                       : (uint32_t)w_row((q * 4 + wave) * S::CopyRows + cr) * (uint32_t)x_bytes + piece * 16;
+      b_off[q] = S::W4 ? (uint32_t)w_row((q * S::Waves + wave) * 32 + (lane >> 1)) * (uint32_t)(K / 2) + half * 16
+                       : (uint32_t)w_row((q * S::Waves + wave) * S::CopyRows + cr) * (uint32_t)x_bytes + piece * 16;
     auto st_a = [&](int buf) { return s_st + buf * S::Stage; };
     auto st_b = [&](int buf) { return s_st + buf * S::Stage + S::StageA; };
     // copy q of a wave's Group, x first
     auto copy = [&](const uint8_t* xb, const uint8_t* wb, int buf, int q) {
-      if (q < ALoads) tile_copy16(xb, a_off[q], tile_lds(st_a(buf) + wave * 1024 + q * 4096));
-      else tile_copy16(wb, b_off[q - ALoads], tile_lds(st_b(buf) + wave * 1024 + (q - ALoads) * 4096));
+      if (q < ALoads) tile_copy16(xb, a_off[q], tile_lds(st_a(buf) + (q * S::Waves + wave) * 1024));
+      else tile_copy16(wb, b_off[q - ALoads], tile_lds(st_b(buf) + ((q - ALoads) * S::Waves + wave) * 1024));
     };
     auto copy_some = [&](int kt, int buf, int from, int to) {
       const uint8_t* xb = x0 + (int64_t)kt * S::Row;
@@ -214,20 +219,23 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
         copy_some(kt, buf, 0, ALoads);
       } else {
 #pragma unroll
-        for (int q = 0; q < ALoads; ++q) *(op_u32x4*)(st_a(buf) + wave * 1024 + q * 4096 + lane * 16) = zero;
+        for (int q = 0; q < ALoads; ++q) *(op_u32x4*)(st_a(buf) + (q * S::Waves + wave) * 1024 + lane * 16) = zero;
       }
       if (S::W4 ? kt * 2 + half < blocks : a_in) {
         copy_some(kt, buf, ALoads, Group);
       } else {
 #pragma unroll
-        for (int q = 0; q < S::BLoads; ++q) *(op_u32x4*)(st_b(buf) + wave * 1024 + q * 4096 + lane * 16) = zero;
+        for (int q = 0; q < S::BLoads; ++q) *(op_u32x4*)(st_b(buf) + (q * S::Waves + wave) * 1024 + lane * 16) = zero;
       }
     };
 
     // this lane's W rows within the tile
     int brow[J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) brow[j] = (GLU ? j * NT + wave * 32 : wave * 32 * J + j * 32) + lr;
+    for (int j = 0; j < J; ++j) brow[j] = (GLU ? j * NT + wn * 32 : wn * 32 * J + j * 32) + lr;
+    // its row blocks of x: every other one where two waves share them, so that a
+    // short tile loads both
+    auto arow = [&](int i) { return (i * S::WavesM + wm) * 32; };
 
     // Scales lie in LDS for ChunkSteps steps at once (K >= 512): a row's scales of
     // one step are 2 to 8 bytes, too few for a load each.  A thread brings whole
@@ -237,23 +245,26 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     // previous row's place, which is unused then, or the 16 bytes in front.
     constexpr int Pieces = C::ScaleBytes / 16;
     tile_bytes16 sc[S::WM ? S::ScaleTurns * Pieces : 1];
-    const uint8_t* sc_src[S::WM ? S::ScaleTurns : 1];
+    uint32_t sc_off[S::WM ? S::ScaleTurns : 1];
+    // whether a wave's 64 rows of turn u are rows of W
+    auto sc_of_w = [&](int u) { return !S::XM || u * S::Threads + wave * 64 < S::N; };
     if constexpr (S::WM) {
 #pragma unroll
       for (int u = 0; u < S::ScaleTurns; ++u) {
-        const int r = min(u * kTlThreads + tid, S::N + (S::XM ? NI * 32 : 0) - 1);
-        sc_src[u] = r < S::N ? ws0 + (uint32_t)w_row(r) * (uint32_t)blocks
-                             : xs0 + (uint32_t)x_row(r - S::N) * (uint32_t)blocks;
+        const int r = min(u * S::Threads + tid, S::N + (S::XM ? NI * S::WavesM * 32 : 0) - 1);
+        sc_off[u] = (uint32_t)(sc_of_w(u) ? w_row(r) : x_row(r - S::N)) * (uint32_t)blocks;
       }
     }
     auto load_scales = [&](int kt) {
       if constexpr (S::WM) {
         const int b0 = kt * S::StepBlocks, n = min(C::ScaleBytes, blocks - b0);
 #pragma unroll
-        for (int u = 0; u < S::ScaleTurns; ++u)
+        for (int u = 0; u < S::ScaleTurns; ++u) {
+          const uint8_t* const base = (sc_of_w(u) ? ws0 : xs0) + b0;
 #pragma unroll
           for (int d = 0; d < Pieces; ++d)
-            sc[u * Pieces + d] = *(const tile_bytes16*)(sc_src[u] + b0 + min(d * 16, n - 16));
+            sc[u * Pieces + d] = *(const tile_bytes16*)(base + min(d * 16, n - 16) + sc_off[u]);
+        }
       }
     };
     auto store_scales = [&](int kt) {
@@ -261,8 +272,8 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
         const int n = min(C::ScaleBytes, blocks - kt * S::StepBlocks);
 #pragma unroll
         for (int u = 0; u < S::ScaleTurns; ++u) {
-          const int r = u * kTlThreads + tid;
-          if (r < S::N + (S::XM ? NI * 32 : 0))
+          const int r = u * S::Threads + tid;
+          if (r < S::N + (S::XM ? NI * S::WavesM * 32 : 0))
 #pragma unroll
             for (int d = 0; d < Pieces; ++d)
               *(tile_bytes16*)(s_sc + 16 + r * S::ScalePitch + min(d * 16, n - 16)) = sc[u * Pieces + d];
@@ -282,7 +293,7 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
           else return *(const uint2*)p;
         };
 #pragma unroll
-        for (int i = 0; i < NI; ++i) sx_n[i] = get(S::N + i * 32 + lr);
+        for (int i = 0; i < NI; ++i) sx_n[i] = get(S::N + arow(i) + lr);
 #pragma unroll
         for (int j = 0; j < J; ++j) sw_n[j] = get(brow[j]);
       } else if constexpr (S::WM) {
@@ -324,7 +335,7 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     auto read = [&](int buf, int ks, int to) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        fx[to][i] = *(const op_u32x4*)(st_a(buf) + tile_at<S::Row>(i * 32 + lr, S::W4 ? 4 * kg + ks : 2 * ks + kg));
+        fx[to][i] = *(const op_u32x4*)(st_a(buf) + tile_at<S::Row>(arow(i) + lr, S::W4 ? 4 * kg + ks : 2 * ks + kg));
       if constexpr (!S::W4) {
 #pragma unroll
         for (int j = 0; j < J; ++j) fw[to][j] = *(const op_u32x4*)(st_b(buf) + tile_at<S::Row>(brow[j], 2 * ks + kg));
@@ -474,17 +485,17 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     // tile costs its instruction fetches.
     constexpr int CW = GLU ? 32 : 32 * J, CS = 32 * J + 4;  // columns of y of a wave; padded stride
     constexpr int LPR = CW / 8, RPI = 64 / LPR;             // lanes per row (8 columns each), rows per pass
-    static_assert(4 * 32 * CS * 4 <= Stages * S::Stage, "the staging fits the stages");
+    static_assert(S::Waves * 32 * CS * 4 <= Stages * S::Stage, "the staging fits the stages");
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // every wave is done with the stages
     const int c8 = (lane % LPR) * 8, rs = lane / LPR;
-    const int col = n0 + wave * CW + c8;
+    const int col = n0 + wn * CW + c8;
     const bool wide = (((uintptr_t)a.y & 15) | (a.ldy & (a.y_f32 ? 3 : 7))) == 0 && col + 8 <= n_out;
     auto out = [&](int i, const float* c) {
       op_f32x4 v[32 / RPI][2];
       int row[32 / RPI];
 #pragma unroll
       for (int q = 0; q < 32 / RPI; ++q) {
-        const int rl = q * RPI + rs, m = i * 32 + rl;
+        const int rl = q * RPI + rs, m = arow(i) + rl;
         row[q] = s_y[m];
         const bool live = s_x[m] >= 0;
 #pragma unroll
@@ -533,7 +544,7 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
     };
     // as many row blocks at once as the stages hold, up to two: one round of
     // latencies for both
-    constexpr int Batch = NI % 2 == 0 && 4 * 2 * 32 * CS * 4 <= Stages * S::Stage ? 2 : 1;
+    constexpr int Batch = NI % 2 == 0 && S::Waves * 2 * 32 * CS * 4 <= Stages * S::Stage ? 2 : 1;
     float* const c = (float*)s_st + wave * (Batch * 32 * CS);
 #pragma unroll 1
     for (int i = 0; i < NI; i += Batch) {
@@ -549,26 +560,16 @@ __global__ __launch_bounds__(kTlThreads, 1) void product_tile_kernel(ProductArgs
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before the next rows overwrite them
     }
   };
-  const int ni = (t.rows + 31) >> 5;
+  const int ni = (t.rows + 32 * S::WavesM - 1) / (32 * S::WavesM);
   if constexpr (C::MaxI == 2) {
     if (ni == 1) run(integral_constant<int, 1>{});
     else run(integral_constant<int, 2>{});
-  } else if constexpr (C::MaxI == 4) {
+  } else {
     switch (ni) {
       case 1: run(integral_constant<int, 1>{}); break;
       case 2: run(integral_constant<int, 2>{}); break;
       case 3: run(integral_constant<int, 3>{}); break;
       default: run(integral_constant<int, 4>{}); break;
-    }
-  } else {
-    switch (ni) {
-      case 1: run(integral_constant<int, 1>{}); break;
-      case 2: run(integral_constant<int, 2>{}); break;
-      case 3:
-      case 4: run(integral_constant<int, 4>{}); break;
-      case 5:
-      case 6: run(integral_constant<int, 6>{}); break;
-      default: run(integral_constant<int, 8>{}); break;
     }
   }
 }
@@ -579,8 +580,8 @@ hipError_t launch_tile_as(const ProductArgs& a, hipStream_t s) {
   const int n_out = GLU ? a.N / 2 : a.N, nt = GLU ? S::N / 2 : S::N;
   const int64_t n_ntiles = (n_out + nt - 1) / nt;
   const int64_t wgs = (op_max_tiles(a, S::M) * n_ntiles + 7) / 8 * 8;
-  if (wgs * kTlThreads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-  return launch_op(product_tile_kernel<AT, WT, GLU, C>, dim3((unsigned)wgs), dim3(kTlThreads), s, a);
+  if (wgs * S::Threads >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
+  return launch_op(product_tile_kernel<AT, WT, GLU, C>, dim3((unsigned)wgs), dim3(S::Threads), s, a);
 }
 
 template <int AT, int WT>
