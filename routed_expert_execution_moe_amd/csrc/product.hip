@@ -232,9 +232,8 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
 template <int AT, int WT>
 static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
   constexpr bool XM = AT == MOE_MXFP4, W4 = !XM && WT == MOE_MXFP4;
-  // the tile kernels address the rows of x of a tile with 32-bit offsets and
-  // read MXFP4 scales 16 at a time
-  if (a.x_ld < (1 << 23) && (WT != MOE_MXFP4 || a.K >= 512)) {
+  // the tile kernels address the rows of x of a tile with 32-bit offsets
+  if (a.x_ld < (1 << 23)) {
     const int64_t n_out = glu ? a.N / 2 : a.N, rows = a.n_rows / a.n_experts;
     auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * ((n_out + n - 1) / n); };
     auto tile = [&](TileKind kind) {

@@ -199,6 +199,8 @@ GEMM_TILES = [  # enough tiles for each of the LDS variants; ends inside steps a
     (1500, 1500, 672), (1090, 2050, 2112),                      # 64 x 128 tiles, several per CU
     (2050, 4100, 544), (2049, 4353, 1568), (2300, 4000, 4192),  # 128 x 128 tiles
     (4100, 4097, 544), (4353, 3900, 1696), (3850, 4352, 4128),  # 256 x 256 tiles
+    # rows of less than 16 scales
+    (500, 1100, 480), (1500, 1500, 32), (2050, 4100, 96), (2100, 4000, 416), (4100, 4097, 256), (4200, 4100, 480),
 ]
 
 
@@ -427,6 +429,13 @@ def test_grouped_bf16_k_of_eights(t, B):
             want, size = OO.grouped_rows(x.v, w, off, R, N)
             y = _grouped(t, B, x, w, off, R, N, "float32")
             _close(y, want, _bound(size, want, K, False), False, K)
+    for K in (8, 40, 72):  # tiles whose only steps end inside
+        for R, N in ((700, 1100), (1300, 4100), (3300, 6700)):
+            log(f"grouped bf16 tiles K={K} R={R} N={N}")
+            off = [0, R // 2, R // 2, R]
+            x, w = Operand(t, rng, R, K, "bf16"), Experts(t, rng, 3, N, K, "bf16")
+            want, size = OO.grouped_rows(x.v, w, off, R, N)
+            _close(_grouped(t, B, x, w, off, R, N, "float32"), want, _bound(size, want, K, False), False, K)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
