@@ -219,16 +219,33 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
 //   faster: 129).  W4A4 4096x4096 at 64 and 128 rows 11.8 small, 12.6 Mid and
 //   16.8, 12.5; bf16 at 128 and 256 rows 29.5, 32.1 and 38.7, 31.9; W4 at 128, 512
 //   rows 23.6, 28 and 57.8, 29; W4A4 up at 1 and 8 tokens 8.2, 10.0 and 17.3, 13.5.
+//   One expert's 8 rows or fewer stay with the small variant, but for W4A4: at 1,
+//   8 and 16 rows of 32768x2048 bf16 27, 32; 30, 32; 37, 32 and W4 15, 25; 20, 25;
+//   26, 25 (W4A4 12.4, 11.0 at one).
 //   Mid is Shared beyond 256 tiles, one per CU.  W4A4 plain at 256 tokens 34
 //   Shared, 55 Deep; 128x4096x4096 (64 tiles) 14.5 Shared, 12.5 Deep.
-//   Half from 257 tiles of its own and 96 rows.  W4A4 plain at 1,024, 2,048 and
-//   4,001 tokens (64, 128, 250 rows) 45 Half, 42 Mid and 58, 63 and 87, 106; bf16
-//   2048x4096x4096 72 Half, 112 Mid.
-//   Big from 256 (GLU 128) tiles of its own and: bf16 192 rows (GLU 128), W4A4 384
-//   (192), W4 768.  Plain at 4,001 and 8,192 tokens (250, 512 rows), Half and Big:
-//   bf16 212, 209 and 383, 310; W4A4 87, 126 and 213, 191; W4 132, 197 and 247, 293.
-//   Up at 2,048 and 4,096 tokens (128, 256 rows), Mid and Big: bf16 250, 222 and
-//   398, 293; W4A4 94, 97 and 152, 127; W4 136, 208 and 237, 275.
+//   Half from 257 tiles of its own and 64 mean rows, W4 96.  Plain at 512 and 1,024
+//   tokens (32, 64 rows), Half and Mid: bf16 86, 84 and 97, 99; W4A4 30, 30 and 36,
+//   41; N = 4096, K = 2048 bf16 407, 408 and 441, 505, W4A4 140, 136 and 151, 170.
+//   Uneven routing (expert e with (e + 1)^-0.6 of the tokens): bf16 98, 87 and 103,
+//   100; W4 55, 50 at 64 rows and 76, 84 at 128.
+//   Big, one expert, by rounds of 256 workgroups: one of Big takes as long as 8/3 of
+//   Half, which share a CU (W4 10/3).  Half and Big, N = K = 4096, 2,048, 3,000 and
+//   4,096 rows (2, 3 and 4 rounds of Half): bf16 71, 93; 108, 94; 138, 108; W4A4 27,
+//   33; 40, 35; 49, 40; W4 66, 87; 98, 91; 134, 109; 3000^2, K = 2048 W4 46, 50;
+//   1300x11000x4096 (4 rounds, 2 of Big) bf16 130, 174.
+//   Big, several experts, from 256 tiles of its own (GLU 128) and these mean rows;
+//   Half (GLU Mid) and Big, even | uneven:
+//     bf16 192, K >= 2048 128.  Plain at 128 and 256 rows 126, 121 | 126, 136; 200,
+//       191 | 213, 171; N = 4096, K = 2048 at 128 rows 609, 479 | 599, 542.
+//     W4A4 384, K >= 2048 192.  Plain at 256 and 384 rows 86, 100 | 86, 85; 154,
+//       124; N = 4096, K = 2048 at 128 and 256 rows 215, 187 | 211, 219; 344, 300 |
+//       363, 296.
+//     W4 768.  N = 4096, K = 2048 at 512 and 1,024 rows 1155, 1172 | 1170, 1142;
+//       2206, 2114 | 2216, 2110.
+//     GLU 128, W4 768.  Up at 64 and 128 rows, bf16 178, 166 | 176, 225; 235, 184 |
+//       247, 233; W4A4 61, 49 | 60, 68; 86, 59 | 86, 82; W4 at 128, 512 and 1,024
+//       rows 128, 121 | 130, 191; 429, 414 | 428, 416; 825, 761 | 826, 753.
 template <int AT, int WT>
 static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
   constexpr bool XM = AT == MOE_MXFP4, W4 = !XM && WT == MOE_MXFP4;
@@ -241,11 +258,16 @@ static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
       else if constexpr (W4) return launch_tile_w4(a, glu, kind, s);
       else return launch_tile_bf16(a, glu, kind, s);
     };
-    const int64_t big = glu ? tiles(256, 128) : tiles(256, 256), mid = tiles(64, 128);
-    if (big >= (glu ? 128 : 256) && rows >= (W4 ? 768 : XM ? (glu ? 192 : 384) : glu ? 128 : 192))
-      return tile(TileKind::kBig);
-    if (!glu && tiles(128, 128) > 256 && rows >= 96) return tile(TileKind::kHalf);
-    if (mid >= (W4 ? 129 : 64)) return tile(mid > 256 ? TileKind::kShared : TileKind::kDeep);
+    const int64_t big = glu ? tiles(256, 128) : tiles(256, 256), half = tiles(128, 128), mid = tiles(64, 128);
+    auto rounds = [](int64_t n) { return (n + 255) / 256; };
+    const bool use_big = a.n_experts == 1 && !glu
+                             ? 3 * rounds(half) > (W4 ? 10 : 8) * rounds(big)
+                             : big >= (glu ? 128 : 256) &&
+                                   rows >= (W4 ? 768 : glu ? 128 : XM ? (a.K < 2048 ? 384 : 192) : a.K < 2048 ? 192 : 128);
+    if (use_big) return tile(TileKind::kBig);
+    if (!glu && half > 256 && rows >= (W4 ? 96 : 64)) return tile(TileKind::kHalf);
+    const bool few = !XM && a.n_experts == 1 && a.n_rows <= 8;
+    if (mid >= (W4 ? 129 : 64) && !few) return tile(mid > 256 ? TileKind::kShared : TileKind::kDeep);
   }
   return glu ? launch_small<AT, WT, true>(a, s) : launch_small<AT, WT, false>(a, s);
 }
