@@ -197,10 +197,13 @@ def test_mx_gemm(t, B, M, N, K, act, out):
 GEMM_TILES = [  # enough tiles for each of the LDS variants; ends inside steps and scale chunks
     (500, 1100, 544), (500, 1100, 1600), (129, 4100, 2080),      # 64 x 128 tiles, one per CU
     (1500, 1500, 672), (1090, 2050, 2112),                      # 64 x 128 tiles, several per CU
-    (2050, 4100, 544), (2049, 4353, 1568), (2300, 4000, 4192),  # 128 x 128 tiles
-    (4100, 4097, 544), (4353, 3900, 1696), (3850, 4352, 4128),  # 256 x 256 tiles
+    (1800, 4100, 544), (1793, 4353, 1568), (1900, 4000, 4192),  # 128 x 128 tiles, two per CU
+    (4100, 4097, 544), (4353, 3900, 1696), (3850, 4352, 4128),  # and more
+    (2050, 4100, 544), (2049, 4353, 1568), (2300, 4000, 4192),  # 256 x 256 tiles (bf16 x MXFP4 128 x 128)
+    (3900, 4050, 544), (3841, 4081, 1696), (4090, 3900, 4128),  # 256 x 256 tiles, one for every CU
     # rows of less than 16 scales
     (500, 1100, 480), (1500, 1500, 32), (2050, 4100, 96), (2100, 4000, 416), (4100, 4097, 256), (4200, 4100, 480),
+    (3900, 4050, 256), (4000, 4081, 480),
 ]
 
 
@@ -376,6 +379,7 @@ def test_grouped_up_and_down(t, B, T, k, E, N, K, fmt):
 GROUPED_TILES = [  # T, k, E, N, K, glu
     (260, 4, 16, 1538, 544, True), (260, 4, 16, 1538, 544, False), (90, 8, 60, 2050, 1120, False),
     (1500, 2, 5, 2050, 1568, True), (1500, 2, 5, 4098, 544, False), (3001, 3, 6, 1026, 2080, True),
+    (1000, 2, 4, 4098, 1568, False), (2000, 2, 4, 4098, 2080, False),
 ]
 
 
