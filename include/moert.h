@@ -520,8 +520,9 @@ typedef struct {
 moe_status moe_grouped_gemm(const moe_grouped_args* args, moe_stream stream);
 
 /* y[t] = sum over ascending j of w[t][j] * p[t*k + j] in fp32, one rounding:
- * moe_merge's sum over rows that the caller holds.  p [T*k][H], H <= 2^30 (F32 or BF16,
- * ldp elements from row to row), w fp32 [T][k], y [T][H] (F32 or BF16, ldy).
+ * moe_merge's sum over rows that the caller holds.  p [T*k][H] (F32 or BF16, ldp
+ * elements from row to row), w fp32 [T][k], y [T][H] (F32 or BF16, ldy); k and
+ * H at most 2^30.
  * ids [T][k] or NULL: pairs with an id outside 0..E-1 are left out (their rows
  * are not read), so a token without any expert gives a row of zeros.
  * Alignment: that of the elements. */

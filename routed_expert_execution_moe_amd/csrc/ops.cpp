@@ -195,7 +195,7 @@ extern "C" moe_status moe_combine_pairs(const void* p, moe_dtype p_dtype, int64_
     const char* me = "moe_combine_pairs";
     if (!is_act(p_dtype) || !is_act(y_dtype))
       return fail(nullptr, MOE_EUNSUPPORTED, "moe_combine_pairs: p and y must be F32 or BF16");
-    if (T < 0 || k < 1 || H < 1 || H > 1 << 30) return bad(me, "T must be >= 0, k >= 1 and H in 1..2^30");
+    if (T < 0 || k < 1 || k > 1 << 30 || H < 1 || H > 1 << 30) return bad(me, "T must be >= 0, k and H in 1..2^30");
     if (ids && E < 1) return bad(me, "E must be >= 1 with ids");
     if (T == 0) return MOE_OK;
     if (!p || !w || !y) return bad(me, "NULL argument");

@@ -155,7 +155,7 @@ def test_group_refusals_and_workspace():
 
 @pytest.mark.parametrize("kw,status", [
     (dict(p_dtype=MX), MOE_EUNSUPPORTED), (dict(y_dtype=9), MOE_EUNSUPPORTED), (dict(T=-1), MOE_EINVAL),
-    (dict(k=0), MOE_EINVAL), (dict(H=0), MOE_EINVAL), (dict(ldp=63), MOE_EINVAL), (dict(ldy=63), MOE_EINVAL),
+    (dict(k=0), MOE_EINVAL), (dict(k=(1 << 30) + 1), MOE_EINVAL), (dict(k=(1 << 31) - 1), MOE_EINVAL), (dict(H=0), MOE_EINVAL), (dict(ldp=63), MOE_EINVAL), (dict(ldy=63), MOE_EINVAL),
     (dict(ids=A, E=0), MOE_EINVAL), (dict(ids=A + 1), MOE_EINVAL), (dict(p=A + 2), MOE_EINVAL),
     (dict(H=(1 << 30) + 1, ldp=1 << 31, ldy=1 << 31), MOE_EINVAL), (dict(w=None), MOE_EINVAL), (dict(w=A + 2), MOE_EINVAL), (dict(T=0, p=None), 0),
 ])
