@@ -455,7 +455,8 @@ moe_status moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_
 /* y[M][N] = x[M][K] * W[N][K]^T with W in MXFP4.  x is BF16 (x_scales NULL;
  * ldx >= K elements from row to row) or MXFP4 (x holds codes, x_scales the
  * scales; ldx must be K).  fp32 accumulation, one rounding to y_dtype (BF16 or
- * F32).  K % 32 == 0, any N; ldy >= N.  MOE_EUNSUPPORTED for other dtypes. */
+ * F32).  K % 32 == 0, K <= 2^30, any N; ldy >= N.  MOE_EUNSUPPORTED for other
+ * dtypes. */
 moe_status moe_mx_gemm(const void* x, moe_dtype x_dtype, const uint8_t* x_scales, int64_t ldx,
                        const uint8_t* w_codes, const uint8_t* w_scales, void* y, moe_dtype y_dtype,
                        int64_t ldy, int32_t M, int32_t N, int32_t K, moe_stream stream);
@@ -493,7 +494,7 @@ moe_status moe_group_pairs(const int32_t* ids, int32_t T, int32_t k, int32_t E, 
  * scales at w_scales + e * ws_stride), so a matrix inside expert banks can be
  * used in place.  w_stride is a multiple of 16 bytes and one expert's matrix
  * stays below 2^31 bytes.  K % 32 == 0 where an operand is MXFP4, else K % 8
- * == 0.  With x_index, the rows of x span less than 2^31 bytes. */
+ * == 0; K <= 2^30.  With x_index, the rows of x span less than 2^31 bytes. */
 typedef struct {
   int32_t n_experts;         /* E (1..1024)                                       */
   int32_t n_rows;            /* positions, >= 0                                   */

@@ -9,6 +9,7 @@ namespace {
 constexpr int64_t kInt32Bytes = (int64_t)1 << 31;
 constexpr int64_t kMaxRows = kInt32Bytes - 4096;  // row counts, rounded up to tiles, stay int32
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int32_t kMaxK = 1 << 30;  // the small kernel's 32-bit cursor runs up to 1,024 past K
 constexpr int64_t kMaxPairs = (int64_t)1 << 24;  // each chunk of pairs sums the counts of all others
 
 int64_t elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
@@ -79,6 +80,7 @@ static moe_status check_product(const char* me, const ProductArgs& a, int x_dtyp
                 std::string(me) + ": x and W must be (BF16, BF16), (BF16, MXFP4) or (MXFP4, MXFP4), y F32 or BF16");
   if (a.n_rows >= kMaxRows) return bad(me, "too many rows");
   if (a.n_rows < 0 || a.n_x < 0 || a.n_y < 0 || a.N < 1 || a.K < 1) return bad(me, "negative or empty size");
+  if (a.K > kMaxK) return bad(me, "K must be at most 2^30");
   if (a.K % (wm ? 32 : 8)) return bad(me, "K must be a multiple of 32 with MXFP4 operands, else of 8");
   if ((glu != 0 && glu != 1) || (glu && a.N % 2)) return bad(me, "glu must be 0 or 1, and N even with it");
   if (a.n_rows == 0) return MOE_OK;

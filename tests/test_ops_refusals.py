@@ -238,3 +238,16 @@ def test_oracle_quantiser():
     x[1, 5], x[2, 40] = np.inf, np.nan
     codes, scales = OO.mx_quantize(x)
     assert scales[1, 0] == 255 and scales[2, 1] == 255 and not codes[1, :16].any() and scales[1, 1] != 255
+
+
+@pytest.mark.parametrize("N,K,status", [(1, (1 << 31) - 32, MOE_EINVAL), (2, (1 << 31) - 896, MOE_EINVAL),
+                                        (1, (1 << 30) + 32, MOE_EINVAL)])
+def test_products_refuse_k_past_the_kernels_cursor(N, K, status):
+    """The few-row kernel's waves step through K by 1,024 in 32 bits.  One or two
+    rows of 4-bit weights stay below 2^31 bytes with a K that such a cursor would pass."""
+    for x in (dict(x_dtype=BF16, ldx=K), dict(x_dtype=MX, xs=A, ldx=K)):
+        assert _gemm(N=N, K=K, M=1, ldy=N, **x) == status
+        assert "2^30" in B.moe_last_error()
+    for x in (dict(x_dtype=BF16), dict(x_dtype=MX, x_scales=A)):
+        assert _grouped(N=N, K=K, n_rows=1, ldx=K, w_dtype=MX, w_scales=A, w_stride=K, ldy=N, **x) == status
+        assert "2^30" in B.moe_last_error()
