@@ -516,11 +516,12 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
     auto out = [&](int i, const float* c) {
       op_f32x4 v[32 / RPI][2];
       int row[32 / RPI];
+      bool live[32 / RPI];
 #pragma unroll
       for (int q = 0; q < 32 / RPI; ++q) {
         const int rl = q * RPI + rs, m = arow(i) + rl;
         row[q] = s_y[m];
-        const bool live = s_x[m] >= 0;
+        live[q] = s_x[m] >= 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           op_f32x4 z = *(const op_f32x4*)&c[rl * CS + c8 + h * 4];
@@ -529,7 +530,7 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
 #pragma unroll
             for (int w = 0; w < 4; ++w) z[w] = op_silu_mul(z[w], u[w]);
           }
-          v[q][h] = live ? z : op_f32x4{0.f, 0.f, 0.f, 0.f};
+          v[q][h] = z;
         }
       }
 #pragma unroll
@@ -538,21 +539,22 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
         const int64_t at = (int64_t)row[q] * a.ldy + col;
         if (wide) {
           if (a.y_f32) {
-            *(op_f32x4*)((float*)a.y + at) = v[q][0];
-            *(op_f32x4*)((float*)a.y + at + 4) = v[q][1];
+            const op_f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            *(op_f32x4*)((float*)a.y + at) = live[q] ? v[q][0] : zero;
+            *(op_f32x4*)((float*)a.y + at + 4) = live[q] ? v[q][1] : zero;
           } else {
             op_u32x4 p;
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-              p[w] = op_bf16(v[q][w >> 1][(w & 1) * 2]) | (uint32_t)op_bf16(v[q][w >> 1][(w & 1) * 2 + 1]) << 16;
-            *(op_u32x4*)((uint16_t*)a.y + at) = p;
+            for (int w = 0; w < 4; ++w) p[w] = op_bf16_pair(v[q][w >> 1][(w & 1) * 2], v[q][w >> 1][(w & 1) * 2 + 1]);
+            *(op_u32x4*)((uint16_t*)a.y + at) = live[q] ? p : op_u32x4{0, 0, 0, 0};
           }
         } else {
 #pragma unroll
           for (int u = 0; u < 8; ++u)
             if (col + u < n_out) {
-              if (a.y_f32) ((float*)a.y)[at + u] = v[q][u >> 2][u & 3];
-              else ((uint16_t*)a.y)[at + u] = op_bf16(v[q][u >> 2][u & 3]);
+              const float z = live[q] ? v[q][u >> 2][u & 3] : 0.f;
+              if (a.y_f32) ((float*)a.y)[at + u] = z;
+              else ((uint16_t*)a.y)[at + u] = op_bf16(z);
             }
         }
       }

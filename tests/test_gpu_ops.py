@@ -704,3 +704,64 @@ def test_layer_streams_and_graph(t, B, fmt):
             assert t.equal(s["y"], got), turn
             s["x"].copy_(keep)
             t.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ the SiLU's range
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("R", [3, 300])
+def test_glu_far_gates(t, B, R, fmt):
+    """silu(gate) * up where exp(-gate) leaves fp32 and up is large enough that the
+    product does not vanish.  The sums are exact (two terms of few bits), so the
+    error is the SiLU's: exp(-|g|/2) (1.5 |g| / 2 + 2) * 2^-24 and used squared,
+    reciprocal, sum and four products under 12 * 2^-24; subnormal results one step."""
+    log(f"glu far gates {fmt} R={R}")
+    act, wt = fmt.split("-")
+    half, K = 128 * 33, 64
+    gates = [(-64, -24), (-64, -8), (-96, 0), (-96, -8), (-64, -64), (-96, -64), (-8, -4), (64, 24), (96, 32), (0, 0)]
+    ups = [1.0, -2.0 ** 60, 2.0 ** 100, 1.5 * 2.0 ** 126]
+    g = np.array([gates[n % len(gates)] for n in range(half)], np.float64)
+    u = np.array([ups[n // len(gates) % len(ups)] for n in range(half)])
+    wide = (g.sum(1) > 0) & (np.abs(u) > 2.0 ** 100)
+    u[wide] = 1.0  # the product would leave fp32
+    w, x = np.zeros((2 * half, K)), np.zeros((R, K))
+    w[:half, :2], w[half:, 0], x[:, :2] = g, u, 1.0
+    if wt == "bf16":
+        wd, wsc = _dev(t, w.astype(np.float32), t.bfloat16)[None], None
+    else:
+        c, s = OO.mx_quantize(w)
+        assert np.array_equal(OO.mx_values(c, s), w)
+        wd, wsc = _dev(t, c)[None], _dev(t, s)[None]
+    if act == "bf16":
+        xd, xs = _dev(t, x.astype(np.float32), t.bfloat16), None
+    else:
+        xd, xs = (_dev(t, a) for a in OO.mx_quantize(x))
+    z = g.sum(1)
+    want = z / (1 + np.exp(-z)) * u
+    for out in (t.float32, t.bfloat16):
+        y = t.full((R, half), 7.0, dtype=out, device="cuda")
+        B.moe_grouped_gemm(xd, wd, _dev(t, np.array([0, R], np.int32)), y, x_scales=xs, w_scales=wsc, glu=True)
+        t.cuda.synchronize()
+        step = 2.0 ** -8 if out == t.bfloat16 else 2.0 ** -24
+        tiny = 2.0 ** -133 if out == t.bfloat16 else 2.0 ** -148
+        tol = ((1.5 * np.abs(z) + 16) * 2.0 ** -24 + step) * np.abs(want) + tiny
+        got = _np(y)
+        bad = ~(np.abs(got - want) <= tol)
+        assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3].tolist(), z[np.argwhere(bad)[:3, 1]],
+                               got[bad][:3], np.broadcast_to(want, bad.shape)[bad][:3])
+
+
+def test_glu_infinite_up(t, B):
+    """An infinite up keeps its row's sign through a gate whose exp(-gate) overflows."""
+    log("glu infinite up")
+    for R, half in ((3, 70), (300, 128 * 33)):
+        w = t.zeros((1, 2 * half, 32), dtype=t.bfloat16, device="cuda")
+        w[0, :half, 0], w[0, half:, 0] = -100.0, float("inf")
+        w[0, half + 1, 0] = -float("inf")
+        x = t.zeros((R, 32), dtype=t.bfloat16, device="cuda")
+        x[:, 0] = 1
+        y = t.empty((R, half), device="cuda")
+        B.moe_grouped_gemm(x, w, _dev(t, np.array([0, R], np.int32)), y, glu=True)
+        t.cuda.synchronize()
+        want = t.full((R, half), -float("inf"), device="cuda")
+        want[:, 1] = float("inf")
+        assert t.equal(y, want)
