@@ -433,6 +433,11 @@ moe_status moe_ctx_timing(moe_ctx* ctx, moe_timing* out, int32_t reset);
  *     base addresses of x and of codes are 16-byte aligned, and a leading
  *     dimension (elements from one row to the next) keeps every row of x so.
  *     y needs the alignment of its element only;
+ *   - a product of BF16 rows takes an MXFP4 weight as a BF16 value: exact, but
+ *     magnitudes from 2^128 on (scales 253 and 254, which the conversion of finite
+ *     values never gives) are infinite;
+ *   - a call that would need more workgroups than one launch may have is refused
+ *     (MOE_EINVAL);
  *   - a HIP failure is returned (MOE_EHIP) but not latched.
  * A call with nothing to compute (no rows) returns MOE_OK. */
 

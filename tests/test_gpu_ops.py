@@ -765,3 +765,23 @@ def test_glu_infinite_up(t, B):
         want = t.full((R, half), -float("inf"), device="cuda")
         want[:, 1] = float("inf")
         assert t.equal(y, want)
+
+
+# ------------------------------------------------------------------ the ends of the formats' ranges
+@pytest.mark.parametrize("M,N", [(4, 70), (600, 4100)])
+def test_mx_gemm_bf16_extremes(t, B, M, N):
+    """Subnormal rows of x and weights count in full; a weight is taken as the bf16
+    value nearest to it, so magnitudes from 2^128 on, which no conversion of finite
+    numbers gives, are infinite.  K equal powers of two: the sums are exact."""
+    log(f"gemm bf16 extremes M={M}")
+    K = 64
+    for xv, code, value, scale in ((2.0 ** -130, 2, 1.0, 254), (2.0 ** -133, 2, 1.0, 254), (2.0 ** 120, 1, .5, 0),
+                                   (2.0 ** 120, 7, 6.0, 0), (2.0 ** -100, 7, 6.0, 252), (2.0 ** -100, 5, 3.0, 253),
+                                   (2.0 ** -100, 6, 4.0, 253), (2.0 ** -100, 6, 4.0, 254)):
+        w = t.full((N, K // 2), code * 17, dtype=t.uint8, device="cuda")
+        s = t.full((N, K // 32), scale, dtype=t.uint8, device="cuda")
+        x = _dev(t, np.full((M, K), xv, np.float32), t.bfloat16)
+        y = t.zeros((M, N), device="cuda")
+        B.moe_mx_gemm(x, w, s, y)
+        big = value * 2.0 ** (scale - 127)
+        assert bool((y == (K * xv * big if big < 2.0 ** 128 else float("inf"))).all()), (xv, code, scale)
