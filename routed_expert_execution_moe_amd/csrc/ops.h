@@ -57,6 +57,7 @@ hipError_t launch_tile_mx(const ProductArgs& a, bool glu, TileKind kind, hipStre
 size_t group_workspace(int64_t pairs, int E);
 hipError_t launch_group_pairs(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* perm,
                               int32_t* ws, hipStream_t s);
+// hipErrorInvalidConfiguration as above
 hipError_t launch_combine_pairs(const void* p, bool p_f32, int64_t ldp, const float* w, const int32_t* ids,
                                 int E, int T, int k, int H, void* y, bool y_f32, int64_t ldy, hipStream_t s);
 

@@ -234,6 +234,7 @@ static hipError_t combine_typed(const uint8_t* p, int64_t ldp, const float* w, c
   const bool vec = H % 4 == 0 && (uintptr_t)p % PB == 0 && ldp % 4 == 0 && (uintptr_t)y % YB == 0 && ldy % 4 == 0;
   const int V = vec ? 4 : 1;
   const dim3 g((H + 64 * V - 1) / (64 * V), std::min((T - 1) / 4 + 1, 65535));
+  if ((int64_t)g.x * 256 >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   return launch_op(vec ? combine_kernel<PF32, YF32, 4> : combine_kernel<PF32, YF32, 1>, g, dim3(256), s, p,
                    ldp, w, ids, E, T, k, H, y, ldy);
 }

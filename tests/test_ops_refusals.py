@@ -251,3 +251,12 @@ def test_products_refuse_k_past_the_kernels_cursor(N, K, status):
     for x in (dict(x_dtype=BF16), dict(x_dtype=MX, x_scales=A)):
         assert _grouped(N=N, K=K, n_rows=1, ldx=K, w_dtype=MX, w_scales=A, w_stride=K, ldy=N, **x) == status
         assert "2^30" in B.moe_last_error()
+
+
+def test_combine_refuses_more_workgroups_than_a_launch_has():
+    """A column a thread (p off the four-column alignment): 2^24 workgroups of 256
+    at H = 2^30, one too many."""
+    f = B.lib().moe_combine_pairs
+    H = 1 << 30
+    assert f(A + 4, F32, H, A, None, 0, 1, 1, H, A, F32, H, None) == MOE_EINVAL
+    assert "workgroups" in B.moe_last_error()
