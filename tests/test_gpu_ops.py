@@ -785,3 +785,84 @@ def test_mx_gemm_bf16_extremes(t, B, M, N):
         B.moe_mx_gemm(x, w, s, y)
         big = value * 2.0 ** (scale - 127)
         assert bool((y == (K * xv * big if big < 2.0 ** 128 else float("inf"))).all()), (xv, code, scale)
+
+
+# ------------------------------------------------------------------ every variant
+GROUPED_VARIANTS = [  # T, k, E, N, K, glu
+    (60, 1, 1, 2090, 544, False), (75, 2, 3, 1000, 1120, False),   # 32 x 32 blocks
+    (180, 1, 1, 2040, 544, False), (150, 2, 2, 1000, 1120, False),  # 64 x 64 blocks
+    (150, 2, 4, 4340, 2080, True), (150, 2, 4, 4340, 4128, True),   # GLU 64 x 256 tiles, scales of more than one chunk
+]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,k,E,N,K,glu", GROUPED_VARIANTS)
+def test_grouped_variants(t, B, T, k, E, N, K, glu, fmt):
+    """Sizes for the variants that no other test's sizes lead to."""
+    test_grouped_tiles(t, B, T, k, E, N, K, glu, fmt)
+
+
+# ------------------------------------------------------------------ large calls
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("pad", [0, 64])
+def test_quantize_large(t, B, dtype, pad):
+    """Inputs of 128 MiB are read past the caches: as many bytes as that and one
+    row less, contiguous and with gaps, against the oracle in some rows and the
+    same rows converted in small calls."""
+    dt = getattr(t, dtype)
+    C = 2048
+    R = (128 << 20) // (C * dt.itemsize)
+    log(f"quantize large {dtype} {R}x{C} pad {pad}")
+    g = t.Generator(device="cuda").manual_seed(21)
+    buf = t.randn(R, C + pad, generator=g, device="cuda")
+    buf *= t.exp2(t.randint(-140, 120, (R, 1), generator=g, device="cuda").float())
+    buf[7, 5], buf[R - 1, C - 1], buf[11, 64:96] = float("inf"), float("nan"), 0.0
+    x = buf.to(dt)[:, :C]
+    rows = [0, 7, 11, R // 2, R - 2, R - 1]
+    want = OO.mx_quantize(_np(x[rows]))
+    for n in (R, R - 1):
+        codes = t.full((n, C // 2), 77, dtype=t.uint8, device="cuda")
+        scales = t.full((n, C // 32), 77, dtype=t.uint8, device="cuda")
+        B.moe_mx_quantize(x[:n], codes, scales)
+        for i in range(0, n, 4096):
+            m = min(4096, n - i)
+            c = t.empty((m, C // 2), dtype=t.uint8, device="cuda")
+            s = t.empty((m, C // 32), dtype=t.uint8, device="cuda")
+            B.moe_mx_quantize(x[i:i + m], c, s)
+            assert t.equal(codes[i:i + m], c) and t.equal(scales[i:i + m], s)
+        live = [r for r in rows if r < n]
+        assert np.array_equal(codes[live].cpu().numpy(), want[0][:len(live)])
+        assert np.array_equal(scales[live].cpu().numpy(), want[1][:len(live)])
+
+
+@pytest.mark.parametrize("T,k,E", [(1 << 17, 8, 256), (1 << 21, 8, 1024)])
+def test_group_pairs_large(t, B, T, k, E):
+    """2^20 pairs, and the 2^24 that a call may have."""
+    log(f"group large {T}x{k} E={E}")
+    rng = np.random.default_rng(k + E)
+    flat = rng.integers(-1, E + 1, T * k).astype(np.int32)
+    key = np.where((flat < 0) | (flat >= E), E, flat).astype(np.int16)
+    order = np.argsort(key, kind="stable").astype(np.int32)
+    off = np.concatenate([[0], np.cumsum(np.bincount(key, minlength=E + 1)[:E])]).astype(np.int32)
+    order[off[-1]:] = -1
+    offsets = t.full((E + 1,), 5, dtype=t.int32, device="cuda")
+    perm = t.full((T * k,), 5, dtype=t.int32, device="cuda")
+    ws = t.empty(B.moe_group_workspace(T, k, E), dtype=t.uint8, device="cuda")
+    B.moe_group_pairs(_dev(t, flat.reshape(T, k)), E, offsets, perm, workspace=ws)
+    t.cuda.synchronize()
+    assert np.array_equal(offsets.cpu().numpy(), off)
+    assert np.array_equal(perm.cpu().numpy(), order)
+
+
+@pytest.mark.parametrize("T,k,H", [(300001, 2, 36), (300001, 1, 7), (9, 3, 1 << 28)])
+def test_combine_large(t, B, T, k, H):
+    """More tokens than the grid's second dimension has rows of workgroups, and
+    rows of p past 2^32 bytes; powers of two, so every sum is exact."""
+    log(f"combine large {T}x{k}x{H}")
+    p = t.ones((T * k, H), dtype=t.bfloat16, device="cuda")
+    p *= t.arange(1, T * k + 1, device="cuda").remainder(61).to(t.bfloat16)[:, None]
+    w = t.full((T, k), 0.5, device="cuda")
+    y = t.full((T, H), 7.0, dtype=t.float32, device="cuda")
+    B.moe_combine_pairs(p, w, y)
+    want = 0.5 * t.arange(1, T * k + 1, device="cuda").remainder(61).view(T, k).sum(1).float()
+    assert bool((y == want[:, None]).all())
