@@ -9,10 +9,10 @@
 // last tile of an expert costs only the blocks it fills and loads every wave
 // alike.
 //
-// K goes in steps of 128 or 64 bytes of a row (64 bf16 or 256 MXFP4 in 128)
-// through a ring of LDS stages that direct-to-LDS loads fill Stages - 1 steps ahead; 16-byte
-// pieces of a row are XOR-swizzled so that the fragment reads of 32 rows spread
-// over the banks.  Fragments are read one slice (a quarter of a step) ahead of
+// K goes in steps of 128 bytes of a row (64 bf16 or 256 MXFP4) through a ring of
+// LDS stages that direct-to-LDS loads fill Stages - 1 steps ahead; 16-byte pieces
+// of a row are XOR-swizzled so that the fragment reads of 32 rows spread over the
+// banks.  Fragments are read one slice (a quarter of a step) ahead of
 // the products that use them, also across the one barrier per step, which sits
 // before a step's last slice: from there on every wave has read the stage, so
 // the next copies may overwrite it.
@@ -52,19 +52,19 @@
 
 namespace moert {
 
-
+constexpr int kTileRow = 128;  // bytes of a row per step
 typedef unsigned int tile_bytes16 __attribute__((ext_vector_type(4), aligned(1)));
 
 template <int AT, int WT>
 struct TileBig {
   static constexpr bool W4 = WT == MOE_MXFP4 && AT == MOE_BF16;
-  static constexpr int Waves = 8, MaxI = 4, J = 2, Row = 128, Stages = W4 ? 3 : 2;
+  static constexpr int Waves = 8, MaxI = 4, J = 2, Stages = W4 ? 3 : 2;
   static constexpr bool Unroll = !W4;
   static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : W4 ? 64 : 32;  // 48: registers spill, 82.4 us for 80.0
 };
 template <int AT, int WT, bool GLU, bool Deep>
 struct TileMid {
-  static constexpr int Waves = 4, MaxI = 2, J = GLU ? 2 : 1, Row = 128;
+  static constexpr int Waves = 4, MaxI = 2, J = GLU ? 2 : 1;
   static constexpr bool Unroll = false;
   static constexpr int Stages = WT == MOE_MXFP4 && AT == MOE_BF16 ? 3 : !Deep ? 2 : GLU ? 3 : 4;
   static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : 64;
@@ -72,7 +72,7 @@ struct TileMid {
 
 template <int AT, int WT>
 struct TileHalf {
-  static constexpr int Waves = 4, MaxI = 4, J = 1, Row = 128, Stages = 2;
+  static constexpr int Waves = 4, MaxI = 4, J = 1, Stages = 2;
   static constexpr bool Unroll = false;
   static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : 48;
 };
@@ -82,9 +82,8 @@ struct TileShape {
   static constexpr bool XM = AT == MOE_MXFP4, WM = WT == MOE_MXFP4, W4 = WM && !XM;
   static constexpr int Waves = C::Waves, WavesM = Waves / 4, Threads = Waves * 64;
   static constexpr int M = 32 * C::MaxI * WavesM, N = 128 * C::J;
-  static constexpr int Row = C::Row, Slices = Row / 32, Parts = Row / 16;  // bytes, slices, 16-byte pieces of a row per step
-  static constexpr int WRow = W4 ? Row / 4 : Row;                         // bytes of a W row per step
-  static_assert(!W4 || Row == 128, "a W4 row's step is two pieces");
+  static constexpr int Row = kTileRow, Parts = Row / 16;  // bytes, 16-byte pieces of a row per step
+  static constexpr int WRow = W4 ? Row / 4 : Row;         // bytes of a W row per step
   static constexpr int StageA = M * Row, StageB = N * WRow, Stage = StageA + StageB;
   static constexpr int CopyRows = 1024 / Row;   // rows of one copy of a wave
   static constexpr int BLoads = StageB / (Waves * 1024);  // per wave and step
@@ -92,7 +91,6 @@ struct TileShape {
   static constexpr int ScaleRows = XM ? M + N : WM ? N : 0;
   static constexpr int ScaleTurns = (ScaleRows + Threads - 1) / Threads;
   static constexpr int StepBlocks = XM ? Row / 16 : 2;   // scales of a row per step
-  static constexpr int ChunkSteps = WM ? C::ScaleBytes / StepBlocks : 1;
 };
 
 // 16 bytes per lane from base + voff to LDS at lds + 16 * lane
@@ -103,13 +101,10 @@ __device__ inline void tile_copy16(const void* base, uint32_t voff, uint32_t lds
 // an LDS address that is the same in every lane, as a scalar
 __device__ inline uint32_t tile_lds(const void* p) { return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)p); }
 
-// swizzle key of row r and place of its 16-byte piece c: two (four) rows of 128
-// (64) bytes fill the 64 banks once, so the key changes from one such group to
-// the next
-template <int Row>
-__device__ inline int tile_key(int r) { return Row == 128 ? (r >> 1) & 7 : (r >> 2) & 3; }
-template <int Row>
-__device__ inline int tile_at(int r, int c) { return r * Row + ((c ^ tile_key<Row>(r)) << 4); }
+// swizzle key of row r and place of its 16-byte piece c: two rows fill the 64
+// banks once, so the key changes from one pair to the next
+__device__ inline int tile_key(int r) { return (r >> 1) & 7; }
+__device__ inline int tile_at(int r, int c) { return r * kTileRow + ((c ^ tile_key(r)) << 4); }
 
 // this wave's reads and all but its newest N copies are done, and every wave is here
 template <int N>
@@ -183,10 +178,10 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
     constexpr int ALoads = (NI * S::WavesM * 32 + S::Waves * S::CopyRows - 1) / (S::Waves * S::CopyRows);
     constexpr int Group = ALoads + S::BLoads;  // copies of one wave per step
 
-    // Copies.  A lane's piece is the same in every row it copies: 4 CopyRows rows
+    // Copies.  A lane's piece is the same in every row it copies: Waves CopyRows rows
     // lie between them, a multiple of the swizzle's period.
     const int cr = lane / S::Parts;
-    const int piece = (lane % S::Parts) ^ tile_key<S::Row>(wave * S::CopyRows + cr);
+    const int piece = (lane % S::Parts) ^ tile_key(wave * S::CopyRows + cr);
     uint32_t a_off[ALoads], b_off[S::BLoads];
 #pragma unroll
     for (int q = 0; q < ALoads; ++q)
@@ -237,7 +232,7 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
     // short tile loads both
     auto arow = [&](int i) { return (i * S::WavesM + wm) * 32; };
 
-    // Scales lie in LDS for ChunkSteps steps at once: a row's scales of one step
+    // Scales lie in LDS for ScaleBytes / StepBlocks steps at once: a row's scales of one step
     // are 2 to 8 bytes, too few for a load each.  A thread brings whole rows,
     // requested a step before they are needed, in pieces of 16.  Those of a row's
     // end overlap the ones before; a row with less than 16 left reads into the
@@ -299,7 +294,7 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
         }
       }
     };
-    // One step's: MXFP4 x MXFP4 the 8 (4) of a row, shifted so that this half's
+    // One step's: MXFP4 x MXFP4 the 8 of a row, shifted so that this half's
     // blocks 2 ks + kg are bytes 0 and 2 of each word, and those past the row's
     // end 1 (their codes are zeros, but zero times a NaN scale is not); W4 that of
     // block kg.
@@ -308,8 +303,7 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
       if constexpr (S::XM) {
         auto get = [&](int r) {
           const uint8_t* p = s_sc + 16 + r * S::ScalePitch + at;
-          if constexpr (S::Slices == 2) return make_uint2(*(const uint32_t*)p, 0);
-          else return *(const uint2*)p;
+          return *(const uint2*)p;
         };
 #pragma unroll
         for (int i = 0; i < NI; ++i) sx_n[i] = get(S::N + arow(i) + lr);
@@ -354,10 +348,10 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
     auto read = [&](int buf, int ks, int to) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        fx[to][i] = *(const op_u32x4*)(st_a(buf) + tile_at<S::Row>(arow(i) + lr, S::W4 ? 4 * kg + ks : 2 * ks + kg));
+        fx[to][i] = *(const op_u32x4*)(st_a(buf) + tile_at(arow(i) + lr, S::W4 ? 4 * kg + ks : 2 * ks + kg));
       if constexpr (!S::W4) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) fw[to][j] = *(const op_u32x4*)(st_b(buf) + tile_at<S::Row>(brow[j], 2 * ks + kg));
+        for (int j = 0; j < J; ++j) fw[to][j] = *(const op_u32x4*)(st_b(buf) + tile_at(brow[j], 2 * ks + kg));
       } else {
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -426,11 +420,9 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
       const bool chunk = S::WM && more && sc_at + S::StepBlocks == C::ScaleBytes;
       if (chunk) load_scales(kt + 1);
       slice(integral_constant<int, 0>{}, buf, 0);
-      if constexpr (S::Slices == 4) {
-        slice(integral_constant<int, 1>{}, buf, 1);
-        slice(integral_constant<int, 2>{}, buf, 0);
-      }
-      const integral_constant<int, S::Slices - 1> last{};
+      slice(integral_constant<int, 1>{}, buf, 1);
+      slice(integral_constant<int, 2>{}, buf, 0);
+      const integral_constant<int, 3> last{};
       if (more) {
         if (steady) tile_sync<(Stages - 2) * Group>();
         else tile_sync<0>();
