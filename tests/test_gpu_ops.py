@@ -866,3 +866,17 @@ def test_combine_large(t, B, T, k, H):
     B.moe_combine_pairs(p, w, y)
     want = 0.5 * t.arange(1, T * k + 1, device="cuda").remainder(61).view(T, k).sum(1).float()
     assert bool((y == want[:, None]).all())
+
+
+@pytest.mark.parametrize("fmt,M,N,K", [("mxfp4-mxfp4", 64, 4096, 1024), ("mxfp4-mxfp4", 256, 1024, 2080),
+                                       ("bf16-mxfp4", 128, 6000, 1024), ("bf16-mxfp4", 64, 16384, 512)])
+def test_one_expert_is_the_dense_product(t, B, fmt, M, N, K):
+    """One group takes the variant of the dense product of its size, so the sums are
+    formed in the same order and every bit agrees; sizes on the rule's borders."""
+    log(f"one expert {fmt} {M}x{N}x{K}")
+    act, wt = fmt.split("-")
+    rng = np.random.default_rng(M + N + K)
+    x, w = Operand(t, rng, M, K, act), Experts(t, rng, 1, N, K, wt)
+    y = t.zeros((M, N), device="cuda")
+    B.moe_mx_gemm(x.t, w.t[0], w.scales[0], y, x_scales=x.scales)
+    assert t.equal(_grouped(t, B, x, w, [0, M], M, N, "float32"), y)
