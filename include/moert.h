@@ -429,8 +429,8 @@ moe_status moe_ctx_timing(moe_ctx* ctx, moe_timing* out, int32_t reset);
  *   - an MXFP4 matrix is codes [rows][cols/2] and scales [rows][cols/32], both
  *     contiguous, in the bank format (OCP MX v1.0 E2M1, low nibble = even
  *     element, one E8M0 scale per 32 elements of a row; scale 255 is NaN);
- *   - codes, scales' matrices and rows of x are addressed in 16-byte pieces:
- *     base addresses of x and of codes are 16-byte aligned, and a leading
+ *   - rows of x and of weights are addressed in 16-byte pieces: base addresses
+ *     of x, of W and of codes are 16-byte aligned, and a leading
  *     dimension (elements from one row to the next) keeps every row of x so.
  *     y needs the alignment of its element only;
  *   - a product of BF16 rows takes an MXFP4 weight as a BF16 value: exact, but

@@ -309,7 +309,10 @@ def moe_ctx_timing(ctx, reset=False) -> dict:
 # `stream` or on that device's current stream.  The checks are host time in
 # front of kernels of a few microseconds: contiguous tensors, the usual case,
 # pass _matrix and _whole in a few attribute reads, and only what does not is
-# looked at for the reason.
+# looked at for the reason.  They serve inference: they write their outputs through
+# plain pointers and record nothing for autograd, whatever requires a gradient.
+# Tensors used on a `stream` other than the one they were allocated on are the
+# caller's to order and to keep (torch.Tensor.record_stream), as with any kernel.
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _U8, _I32, _BF16, _F32 = (torch.uint8,), (torch.int32,), (torch.bfloat16,), (torch.float32,)
 _INT = 1 << 31
@@ -374,7 +377,7 @@ def _call(where, fn, tensors, stream, *args):
 
 
 def moe_mx_quantize(x, codes, scales, stream=None):
-    """x [R, C] f32 or bf16 (rows may be strided) -> codes uint8 [R, C/2], scales uint8 [R, C/32]."""
+    """x [R, C] f32 or bf16 (rows may be strided) -> codes uint8 [R, C/2], scales uint8 [R, C/32].  No gradient."""
     me = "moe_mx_quantize"
     R, C, ld = _matrix(me, "x", x, _FLOATS)
     _need(C % 32 == 0, me, "the columns must be a multiple of 32")
@@ -385,7 +388,7 @@ def moe_mx_quantize(x, codes, scales, stream=None):
 
 
 def moe_mx_dequantize(codes, scales, y, stream=None):
-    """codes uint8 [R, C/2], scales uint8 [R, C/32] -> y [R, C] f32 or bf16 (rows may be strided)."""
+    """codes uint8 [R, C/2], scales uint8 [R, C/32] -> y [R, C] f32 or bf16 (rows may be strided).  No gradient."""
     me = "moe_mx_dequantize"
     R, C, ld = _matrix(me, "y", y, _FLOATS)
     _need(C % 32 == 0, me, "the columns must be a multiple of 32")
@@ -409,7 +412,7 @@ def _rows_operand(me, x, x_scales):
 
 def moe_mx_gemm(x, w_codes, w_scales, y, x_scales=None, stream=None):
     """y [M, N] (f32 or bf16) = x W^T, W as codes uint8 [N, K/2] and scales uint8
-    [N, K/32]; x bf16 [M, K], or codes uint8 [M, K/2] with x_scales [M, K/32]."""
+    [N, K/32]; x bf16 [M, K], or codes uint8 [M, K/2] with x_scales [M, K/32].  No gradient."""
     me = "moe_mx_gemm"
     M, K, x_dtype, ldx = _rows_operand(me, x, x_scales)
     _need(K % 32 == 0, me, "K must be a multiple of 32")
@@ -450,7 +453,7 @@ def moe_grouped_gemm(x, w, offsets, y, x_scales=None, w_scales=None, x_index=Non
     x bf16 [n_x, K] or codes [n_x, K/2] with x_scales; w bf16 [E, N, K] or codes
     [E, N, K/2] with w_scales [E, N, K/32] (any stride from expert to expert);
     y [n_y, N], or [n_y, N/2] with glu; x_index, y_index int32 [n_rows].  The
-    positions are those of an index, else the rows of x."""
+    positions are those of an index, else the rows of x.  No gradient."""
     me = "moe_grouped_gemm"
     n_x, K, x_dtype, ldx = _rows_operand(me, x, x_scales)
     row, dtypes = (K, _BF16) if w_scales is None else (K // 2, _U8)
@@ -490,7 +493,7 @@ def moe_grouped_gemm(x, w, offsets, y, x_scales=None, w_scales=None, x_index=Non
 
 def moe_combine_pairs(p, w, y, ids=None, n_experts=0, stream=None):
     """y [T, H] = sum over j of w[t, j] * p[t*k + j]; p [T*k, H], w f32 [T, k];
-    with ids int32 [T, k], pairs outside 0..n_experts-1 are left out."""
+    with ids int32 [T, k], pairs outside 0..n_experts-1 are left out.  No gradient."""
     me = "moe_combine_pairs"
     T, k, ld = _matrix(me, "w", w, _F32)
     _need(T < 2 or ld == k, me, "w must be contiguous")

@@ -10,9 +10,12 @@
 // the e2m1 grid with ties to even and the saturation at 6 are the gfx950
 // scaled convert; the sign of what rounded to zero is taken off afterwards.
 //
-// HBM bounds both ways: 32768 x 4096 fp32 to MXFP4 104 us (5.8 TB/s), back 117 us
-// (5.2 TB/s; a plain copy reaches 5.1).  Four rows a thread at once were slower (130
-// us), and so were stores past the caches (back: 211 us).
+// HBM bounds both ways: 32768 x 4096 fp32 to MXFP4 110 us (5.5 TB/s), back 105-117
+// us (5.2-5.8 TB/s; a plain copy reaches 5.1).  Four rows a thread at once were
+// slower (130 us), and so were stores past the caches (back: 211 us).  A workgroup
+// takes one row at a time, 2048 columns of it, so narrow rows leave lanes without
+// work: 32008 x 768 bf16 16.8 us for 12.2 at the copy rate, 65536 x 64 fp32 30.7
+// for 3.7.
 #include "ops.h"
 
 namespace moert {

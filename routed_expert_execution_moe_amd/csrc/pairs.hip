@@ -10,7 +10,10 @@
 // each chunk's histogram to the workspace and the second sums, per expert, the
 // histograms before its own chunk and all of them, sixteen loads in flight (one
 // after the other they took 15 of 22 us at 65,536 pairs and 256 experts).
-// Latency bounds it: 3.4 us for 64 pairs, 7 for 4,096, 3.3 + 7.2 for 65,536.
+// Latency bounds it: 3.4 us for 64 pairs, 7 for 4,096, 3.3 + 7.1 for 65,536.  Past
+// that the second launch's sums grow with the square of the chunks: with 256 (1,024)
+// experts 14.8 (25) us at 2^18 pairs, 38 (70) at 2^20, 3.6 (9.6) ms at the 2^24 that
+// a call may have.
 #include "ops.h"
 
 namespace moert {

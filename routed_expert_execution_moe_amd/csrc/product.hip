@@ -18,11 +18,15 @@
 //                   are one 16-byte piece under one scale
 //   MXFP4 x MXFP4   lane group g: k = 32g + [0,32), the scaled MFMA's own order
 //
-// One token against 4096 x 4096 in MXFP4 (8.9 MB) takes 5.8 us of kernel and
-// eight tokens of the same 7.7, five and six of them launch, first loads and the
-// waves' sums; 64 x 4096 x 4096 takes 15.3 us in 32 x 32 blocks.  What bounds it
-// past a few rows is its loads: fragments come through the vector cache once
-// per wave, (MI + NB) of them per MI*NB products.
+// One token against 4096 x 4096 in MXFP4 (8.9 MB) takes 5.6 us of kernel and
+// eight tokens of the same 7.6; 64 x 4096 x 4096 takes 15.2 us in 32 x 32 blocks.
+// Clocks of a workgroup (medians): one token of the above: 1,100 to find its tile,
+// 250 for its rows, 6,800 for a wave's four turns, 1,100 for the sums and 1,000 for
+// the store; 333 x 2040 x 2080 in 64 x 64 blocks (15.5 us): 900, 500, 17,200 for
+// three turns, 4,600 and 9,000, since one wave stores the whole block.  What bounds
+// the turns past a few rows is their loads: fragments come through the vector
+// cache once per wave, (MI + NB) of them per MI*NB products, and with W in 4 bits
+// each of x is four times one of W.
 #include <type_traits>
 
 #include "ops.h"
@@ -205,7 +209,8 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
   const int64_t n_blocks = ((GLU ? a.N / 2 : a.N) + 15) / 16;
   // 16-row blocks while those of W still fill the chip's CUs once: 32 rows of
   // 2048x768 bf16 take 5.3 us in 16 x 16 blocks and 7.6 in 32 x 32, 128 rows of
-  // 4096x4096 61 and 34 us (29.5 in 64 x 64)
+  // 4096x4096 61 and 34 us (29.5 in 64 x 64).  For 16 rows either may be the faster:
+  // W4 4096x4096 8.8 and 12.0, 8192x4096 14.1 and 12.3.
   if (avg <= 16 || op_max_tiles(a, 16) * n_blocks <= 512) return launch_small_as<AT, WT, GLU, 1, 1>(a, s);
   if (avg <= 64 || op_max_tiles(a, 32) * n_blocks <= 512) return launch_small_as<AT, WT, GLU, 2, 2>(a, s);
   return launch_small_as<AT, WT, GLU, 4, GLU ? 2 : 4>(a, s);
@@ -221,12 +226,17 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
 //   rows 23.6, 28 and 57.8, 29; W4A4 up at 1 and 8 tokens 8.2, 10.0 and 17.3, 13.5.
 //   One expert's 8 rows or fewer stay with the small variant, but for W4A4: at 1,
 //   8 and 16 rows of 32768x2048 bf16 27, 32; 30, 32; 37, 32 and W4 15, 25; 20, 25;
-//   26, 25 (W4A4 12.4, 11.0 at one).
+//   26, 25 (W4A4 12.4, 11.0 at one).  Not so several experts, though with weights
+//   from memory the small variant is often the faster there too, bf16's above all;
+//   Mid and small, eight experts of one row each: bf16 4096x2048 37, 28; 8192x4096
+//   124, 87; 8192x1024 27, 30; GLU 16384x4096 283, 171; W4 25, 18; 52, 52; 17, 22;
+//   66, 84.
 //   Mid is Shared beyond 256 tiles, one per CU.  W4A4 plain at 256 tokens 34
 //   Shared, 55 Deep; 128x4096x4096 (64 tiles) 14.5 Shared, 12.5 Deep.
 //   Half from 257 tiles of its own and 64 mean rows, W4 96.  Plain at 512 and 1,024
 //   tokens (32, 64 rows), Half and Mid: bf16 86, 84 and 97, 99; W4A4 30, 30 and 36,
 //   41; N = 4096, K = 2048 bf16 407, 408 and 441, 505, W4A4 140, 136 and 151, 170.
+//   With K = 256 Big loses up to 15 %: plain, N = 2048, 4,001 tokens bf16 85, 99.
 //   Uneven routing (expert e with (e + 1)^-0.6 of the tokens): bf16 98, 87 and 103,
 //   100; W4 55, 50 at 64 rows and 76, 84 at 128.
 //   Big, one expert, by rounds of 256 workgroups: one of Big takes as long as 8/3 of

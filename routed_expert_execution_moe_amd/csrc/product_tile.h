@@ -29,7 +29,7 @@
 // Shapes.  Big, 256 x 256 with eight waves and two stages: a wave reads (NI + 2)
 // fragments from LDS per 2 NI products, 0.75 at NI = 4, and two waves on a SIMD fill
 // each other's waits (four waves with 128 x 2 blocks read 0.63 and leave one wave
-// alone with its own: W4A4 8192 x 4096 x 4096 86.4 us, eight 80.0; bf16 222 and 215).
+// alone with its own: W4A4 8192 x 4096 x 4096 86.4 us, eight 80.0 then; bf16 222 and 215).
 // Half, 128 x 128, and Mid, 64 x 128 (GLU 64 x 256), with four waves, for products
 // whose larger tiles would leave CUs without one or spend their time before and
 // after a short K.  They stay within 80 KB of LDS, so that one workgroup's first
@@ -37,13 +37,14 @@
 // CU to itself, where there are too few tiles to share one, and so has every GLU
 // tile but W4's.
 //
-// 8192 x 4096 x 4096 takes 80 us with MXFP4 operands (3.4 PFLOP/s) and 215 us with
-// bf16 (1.28).  A Big tile's time in clocks, four waves, 4096 x 4096 x 4096, W4A4:
-// 33,000 of products within a loop of 53,000, whose rest waits for copies and
-// fragments; 20,000 while all CUs write their tiles at once; 7,600 until the first
-// stage is there.  Steps of 64 bytes in four stages hide the waits of one tile
-// alone better (1.04 against 1.11 us per 128 bytes of bf16), but asking for half
-// cache lines costs more with all CUs at work (119 against 113 us).
+// 8192 x 4096 x 4096 takes 74-79 us with MXFP4 operands (3.5-3.7 PFLOP/s)
+// and 208-217 us with bf16 (1.27-1.32).  A Big tile's time in clocks, 4096 x
+// 4096 x 4096, W4A4: 1,300 to find it, 1,300 for its rows, 4,500 until the first stage
+// is there; 33,000 of products within a loop of 48,200, whose rest waits for copies
+// and fragments; 10,000 while all CUs write their tiles at once.  Steps of 64 bytes
+// in four stages, tried with four waves, hide the waits of one tile alone better
+// (1.04 against 1.11 us per 128 bytes of bf16), but asking for half cache lines costs
+// more with all CUs at work (119 against 113 us).
 #pragma once
 
 #include <type_traits>
@@ -60,7 +61,8 @@ struct TileBig {
   static constexpr bool W4 = WT == MOE_MXFP4 && AT == MOE_BF16;
   static constexpr int Waves = 8, MaxI = 4, J = 2, Stages = W4 ? 3 : 2;
   static constexpr bool Unroll = !W4;
-  static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : W4 ? 64 : 32;  // 48: registers spill, 82.4 us for 80.0
+  // W4A4: 48 spills registers within the loop, 82.4 us for 80.0 (32: three, one with GLU, outside of it)
+  static constexpr int ScaleBytes = WT != MOE_MXFP4 ? 0 : W4 ? 64 : 32;
 };
 template <int AT, int WT, bool GLU, bool Deep>
 struct TileMid {
