@@ -236,7 +236,6 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
 //   Half from 257 tiles of its own and 64 mean rows, W4 96.  Plain at 512 and 1,024
 //   tokens (32, 64 rows), Half and Mid: bf16 86, 84 and 97, 99; W4A4 30, 30 and 36,
 //   41; N = 4096, K = 2048 bf16 407, 408 and 441, 505, W4A4 140, 136 and 151, 170.
-//   With K = 256 Big loses up to 15 %: plain, N = 2048, 4,001 tokens bf16 85, 99.
 //   Uneven routing (expert e with (e + 1)^-0.6 of the tokens): bf16 98, 87 and 103,
 //   100; W4 55, 50 at 64 rows and 76, 84 at 128.
 //   Big, one expert, by rounds of 256 workgroups: one of Big takes as long as 8/3 of
@@ -247,12 +246,17 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
 //   Big, several experts, from 256 tiles of its own (GLU 128) and these mean rows;
 //   Half (GLU Mid) and Big, even | uneven:
 //     bf16 192, K >= 2048 128.  Plain at 128 and 256 rows 126, 121 | 126, 136; 200,
-//       191 | 213, 171; N = 4096, K = 2048 at 128 rows 609, 479 | 599, 542.
+//       191 | 213, 171; N = 4096, K = 2048 at 128 rows 609, 479 | 599, 542.  With
+//       K = 256 Big loses: N = 2048 at 250 rows 85, 99.
 //     W4A4 384, K >= 2048 192.  Plain at 256 and 384 rows 86, 100 | 86, 85; 154,
 //       124; N = 4096, K = 2048 at 128 and 256 rows 215, 187 | 211, 219; 344, 300 |
 //       363, 296.
 //     W4 768.  N = 4096, K = 2048 at 512 and 1,024 rows 1155, 1172 | 1170, 1142;
 //       2206, 2114 | 2216, 2110.
+//     One expert, GLU, W4A4: from 65 tiles, where Mid's need a second round.  Mid and
+//       Big at 64, 66, 96 and 128 tiles: 19.8, 31.2; 33.6, 31.6; 34.6, 31.8; 36.4, 32.1
+//       (512x8192x4096, 512x8448x4096, 768x8192x4096, 1024x8192x4096); bf16 at 96 and
+//       112 80, 92 and 81, 87.
 //     GLU 128, W4 768.  Up at 64 and 128 rows, bf16 178, 166 | 176, 225; 235, 184 |
 //       247, 233; W4A4 61, 49 | 60, 68; 86, 59 | 86, 82; W4 at 128, 512 and 1,024
 //       rows 128, 121 | 130, 191; 429, 414 | 428, 416; 825, 761 | 826, 753.
@@ -272,7 +276,7 @@ static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
     auto rounds = [](int64_t n) { return (n + 255) / 256; };
     const bool use_big = a.n_experts == 1 && !glu
                              ? 3 * rounds(half) > (W4 ? 10 : 8) * rounds(big)
-                             : big >= (glu ? 128 : 256) &&
+                             : big >= (!glu ? 256 : XM && a.n_experts == 1 ? 65 : 128) &&
                                    rows >= (W4 ? 768 : glu ? 128 : XM ? (a.K < 2048 ? 384 : 192) : a.K < 2048 ? 192 : 128);
     if (use_big) return tile(TileKind::kBig);
     if (!glu && half > 256 && rows >= (W4 ? 96 : 64)) return tile(TileKind::kHalf);
