@@ -48,12 +48,13 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
 // x_dtype / w_dtype as in moe_grouped_gemm; hipErrorInvalidConfiguration when
 // the product needs more workgroups than a launch may have
 hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool glu, hipStream_t s);
-// its variants that stage tiles in LDS (product_tile.h), one source file per
-// pair of types
-enum class TileKind { kBig, kHalf, kDeep, kShared };
-hipError_t launch_tile_bf16(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);
-hipError_t launch_tile_w4(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);
-hipError_t launch_tile_mx(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s);
+// Its variants: the streaming one of product.hip in blocks of 16, 32 and 64 rows, and
+// the ones that stage tiles in LDS (product_tile.h), one source file per pair of types.
+// A gate/up product has one 64-row tile: Shared with W4, else Deep.
+enum class ProductVariant { kSmall16, kSmall32, kSmall64, kDeep, kShared, kHalf, kBig };
+hipError_t launch_tile_bf16(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s);
+hipError_t launch_tile_w4(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s);
+hipError_t launch_tile_mx(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s);
 size_t group_workspace(int64_t pairs, int E);
 hipError_t launch_group_pairs(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* perm,
                               int32_t* ws, hipStream_t s);

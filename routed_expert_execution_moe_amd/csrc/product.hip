@@ -202,20 +202,6 @@ static hipError_t launch_small_as(const ProductArgs& a, hipStream_t s) {
   return launch_op(product_small_kernel<AT, WT, GLU, MI, NB>, dim3((unsigned)wgs), dim3(kSmWaves * 64), s, a);
 }
 
-template <int AT, int WT, bool GLU>
-static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
-  const int groups = std::min(a.n_experts, a.n_rows);
-  const int avg = (a.n_rows + groups - 1) / groups;
-  const int64_t n_blocks = ((GLU ? a.N / 2 : a.N) + 15) / 16;
-  // 16-row blocks while those of W still fill the chip's CUs once: 32 rows of
-  // 2048x768 bf16 take 5.3 us in 16 x 16 blocks and 7.6 in 32 x 32, 128 rows of
-  // 4096x4096 61 and 34 us (29.5 in 64 x 64).  For 16 rows either may be the faster:
-  // W4 4096x4096 8.8 and 12.0, 8192x4096 14.1 and 12.3.
-  if (avg <= 16 || op_max_tiles(a, 16) * n_blocks <= 512) return launch_small_as<AT, WT, GLU, 1, 1>(a, s);
-  if (avg <= 64 || op_max_tiles(a, 32) * n_blocks <= 512) return launch_small_as<AT, WT, GLU, 2, 2>(a, s);
-  return launch_small_as<AT, WT, GLU, 4, GLU ? 2 : 4>(a, s);
-}
-
 // Which variant, by the tiles that a call can make at most and by the mean rows
 // of an expert (us on MI355X; "up" is a GLU product of N = 1536, K = 2048 over 128
 // experts, "plain" one without GLU of N = 2048, K = 768, both with 8 experts a
@@ -261,29 +247,49 @@ static hipError_t launch_small(const ProductArgs& a, hipStream_t s) {
 //       247, 233; W4A4 61, 49 | 60, 68; 86, 59 | 86, 82; W4 at 128, 512 and 1,024
 //       rows 128, 121 | 130, 191; 429, 414 | 428, 416; 825, 761 | 826, 753.
 template <int AT, int WT>
-static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
+static ProductVariant choose(const ProductArgs& a, bool glu) {
   constexpr bool XM = AT == MOE_MXFP4, W4 = !XM && WT == MOE_MXFP4;
+  const int64_t n_out = glu ? a.N / 2 : a.N, rows = a.n_rows / a.n_experts;
+  auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * ((n_out + n - 1) / n); };
   // the tile kernels address the rows of x of a tile with 32-bit offsets
   if (a.x_ld < (1 << 23)) {
-    const int64_t n_out = glu ? a.N / 2 : a.N, rows = a.n_rows / a.n_experts;
-    auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * ((n_out + n - 1) / n); };
-    auto tile = [&](TileKind kind) {
-      if constexpr (XM) return launch_tile_mx(a, glu, kind, s);
-      else if constexpr (W4) return launch_tile_w4(a, glu, kind, s);
-      else return launch_tile_bf16(a, glu, kind, s);
-    };
     const int64_t big = glu ? tiles(256, 128) : tiles(256, 256), half = tiles(128, 128), mid = tiles(64, 128);
     auto rounds = [](int64_t n) { return (n + 255) / 256; };
     const bool use_big = a.n_experts == 1 && !glu
                              ? 3 * rounds(half) > (W4 ? 10 : 8) * rounds(big)
                              : big >= (!glu ? 256 : XM && a.n_experts == 1 ? 65 : 128) &&
                                    rows >= (W4 ? 768 : glu ? 128 : XM ? (a.K < 2048 ? 384 : 192) : a.K < 2048 ? 192 : 128);
-    if (use_big) return tile(TileKind::kBig);
-    if (!glu && half > 256 && rows >= (W4 ? 96 : 64)) return tile(TileKind::kHalf);
+    if (use_big) return ProductVariant::kBig;
+    if (!glu && half > 256 && rows >= (W4 ? 96 : 64)) return ProductVariant::kHalf;
     const bool few = !XM && a.n_experts == 1 && a.n_rows <= 8;
-    if (mid >= (W4 ? 129 : 64) && !few) return tile(mid > 256 ? TileKind::kShared : TileKind::kDeep);
+    if (mid >= (W4 ? 129 : 64) && !few)
+      return W4 || (!glu && mid > 256) ? ProductVariant::kShared : ProductVariant::kDeep;
   }
-  return glu ? launch_small<AT, WT, true>(a, s) : launch_small<AT, WT, false>(a, s);
+  // 16-row blocks while those of W still fill the chip's CUs once: 32 rows of
+  // 2048x768 bf16 take 5.3 us in 16 x 16 blocks and 7.6 in 32 x 32, 128 rows of
+  // 4096x4096 61 and 34 us (29.5 in 64 x 64).  For 16 rows either may be the faster:
+  // W4 4096x4096 8.8 and 12.0, 8192x4096 14.1 and 12.3.
+  const int groups = std::min(a.n_experts, a.n_rows);
+  const int avg = (a.n_rows + groups - 1) / groups;
+  if (avg <= 16 || tiles(16, 16) <= 512) return ProductVariant::kSmall16;
+  if (avg <= 64 || tiles(32, 16) <= 512) return ProductVariant::kSmall32;
+  return ProductVariant::kSmall64;
+}
+
+template <int AT, int WT, bool GLU>
+static hipError_t launch_small(const ProductArgs& a, ProductVariant v, hipStream_t s) {
+  if (v == ProductVariant::kSmall16) return launch_small_as<AT, WT, GLU, 1, 1>(a, s);
+  if (v == ProductVariant::kSmall32) return launch_small_as<AT, WT, GLU, 2, 2>(a, s);
+  return launch_small_as<AT, WT, GLU, 4, GLU ? 2 : 4>(a, s);
+}
+
+template <int AT, int WT>
+static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
+  const ProductVariant v = choose<AT, WT>(a, glu);
+  if (v <= ProductVariant::kSmall64) return glu ? launch_small<AT, WT, true>(a, v, s) : launch_small<AT, WT, false>(a, v, s);
+  if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, v, s);
+  else if constexpr (WT == MOE_MXFP4) return launch_tile_w4(a, glu, v, s);
+  else return launch_tile_bf16(a, glu, v, s);
 }
 
 hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool glu, hipStream_t s) {
@@ -292,4 +298,21 @@ hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool g
                               : launch_typed<MOE_BF16, MOE_BF16>(a, glu, s);
 }
 
+static ProductVariant product_variant(const ProductArgs& a, int x_dtype, int w_dtype, bool glu) {
+  if (x_dtype == MOE_MXFP4) return choose<MOE_MXFP4, MOE_MXFP4>(a, glu);
+  return w_dtype == MOE_MXFP4 ? choose<MOE_BF16, MOE_MXFP4>(a, glu) : choose<MOE_BF16, MOE_BF16>(a, glu);
+}
+
 }  // namespace moert
+
+// The rule's choice for a product of contiguous rows, as a number: the tests check
+// that their sizes reach every variant.  Host arithmetic only.
+extern "C" int moert_product_variant(int x_dtype, int w_dtype, int glu, int n_experts, int n_rows, int N, int K) {
+  moert::ProductArgs a{};
+  a.x_ld = x_dtype == MOE_MXFP4 ? K / 2 : (int64_t)K * 2;
+  a.n_experts = n_experts;
+  a.n_rows = n_rows;
+  a.N = N;
+  a.K = K;
+  return (int)moert::product_variant(a, x_dtype, w_dtype, glu != 0);
+}

@@ -604,16 +604,16 @@ hipError_t launch_tile_as(const ProductArgs& a, hipStream_t s) {
 }
 
 template <int AT, int WT>
-hipError_t launch_tile(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s) {
+hipError_t launch_tile(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s) {
   constexpr bool W4 = AT == MOE_BF16 && WT == MOE_MXFP4;
-  if (kind == TileKind::kHalf && !glu) return launch_tile_as<AT, WT, false, TileHalf<AT, WT>>(a, s);
-  if (kind == TileKind::kBig)
+  if (v == ProductVariant::kBig)
     return glu ? launch_tile_as<AT, WT, true, TileBig<AT, WT>>(a, s) : launch_tile_as<AT, WT, false, TileBig<AT, WT>>(a, s);
   // W4's stages are small enough for both at once; the other formats' GLU
   // tiles are too large to share a CU
   if (glu) return launch_tile_as<AT, WT, true, TileMid<AT, WT, true, !W4>>(a, s);
+  if (v == ProductVariant::kHalf) return launch_tile_as<AT, WT, false, TileHalf<AT, WT>>(a, s);
   if constexpr (!W4)
-    if (kind == TileKind::kDeep) return launch_tile_as<AT, WT, false, TileMid<AT, WT, false, true>>(a, s);
+    if (v == ProductVariant::kDeep) return launch_tile_as<AT, WT, false, TileMid<AT, WT, false, true>>(a, s);
   return launch_tile_as<AT, WT, false, TileMid<AT, WT, false, false>>(a, s);
 }
 

@@ -3,8 +3,8 @@
 
 namespace moert {
 
-hipError_t launch_tile_w4(const ProductArgs& a, bool glu, TileKind kind, hipStream_t s) {
-  return launch_tile<MOE_BF16, MOE_MXFP4>(a, glu, kind, s);
+hipError_t launch_tile_w4(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s) {
+  return launch_tile<MOE_BF16, MOE_MXFP4>(a, glu, v, s);
 }
 
 }  // namespace moert

@@ -260,3 +260,26 @@ def test_combine_refuses_more_workgroups_than_a_launch_has():
     H = 1 << 30
     assert f(A + 4, F32, H, A, None, 0, 1, 1, H, A, F32, H, None) == MOE_EINVAL
     assert "workgroups" in B.moe_last_error()
+
+
+def test_gpu_sizes_reach_every_product_variant():
+    """The rule that picks a product's kernel, on the sizes of the GPU tests: every
+    kernel of every pair of types has one."""
+    from tests import test_gpu_ops as G
+    f = B.lib().moert_product_variant
+    f.argtypes, f.restype = [ctypes.c_int] * 7, ctypes.c_int
+    types = {"bf16-bf16": (BF16, BF16), "bf16-mxfp4": (BF16, MX), "mxfp4-mxfp4": (MX, MX)}
+    names = ["small16", "small32", "small64", "deep", "shared", "half", "big"]
+    got = set()
+    for fmt in G.FORMATS:
+        calls = [(glu, E, T * k, N, K) for T, k, E, N, K in G.GROUPED for glu in (0, 1)]
+        calls += [(int(glu), E, T * k, N, K) for T, k, E, N, K, glu in G.GROUPED_TILES + G.GROUPED_VARIANTS]
+        if fmt != "bf16-bf16":
+            calls += [(0, 1, M, N, K) for M, N, K in G.GEMM + G.GEMM_TILES]
+        got |= {(fmt, c[0], names[f(*types[fmt], *c)]) for c in calls}
+    want = set()
+    for fmt in G.FORMATS:
+        w4 = fmt == "bf16-mxfp4"
+        want |= {(fmt, 0, n) for n in names if not (w4 and n == "deep")}
+        want |= {(fmt, 1, n) for n in ("small16", "small32", "small64", "shared" if w4 else "deep", "big")}
+    assert got == want, (sorted(want - got), sorted(got - want))
