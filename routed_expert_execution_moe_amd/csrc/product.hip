@@ -306,8 +306,9 @@ static ProductVariant product_variant(const ProductArgs& a, int x_dtype, int w_d
 }  // namespace moert
 
 // The rule's choice for a product of contiguous rows, as a number: the tests check
-// that their sizes reach every variant.  Host arithmetic only.
+// that their sizes reach every variant.  Host arithmetic only; -1 for empty sizes.
 extern "C" int moert_product_variant(int x_dtype, int w_dtype, int glu, int n_experts, int n_rows, int N, int K) {
+  if (n_experts < 1 || n_rows < 1 || N < 1 || K < 1) return -1;
   moert::ProductArgs a{};
   a.x_ld = x_dtype == MOE_MXFP4 ? K / 2 : (int64_t)K * 2;
   a.n_experts = n_experts;

@@ -270,6 +270,7 @@ def test_gpu_sizes_reach_every_product_variant():
     f.argtypes, f.restype = [ctypes.c_int] * 7, ctypes.c_int
     types = {"bf16-bf16": (BF16, BF16), "bf16-mxfp4": (BF16, MX), "mxfp4-mxfp4": (MX, MX)}
     names = ["small16", "small32", "small64", "deep", "shared", "half", "big"]
+    assert f(BF16, BF16, 0, 0, 8, 64, 64) == -1
     got = set()
     for fmt in G.FORMATS:
         calls = [(glu, E, T * k, N, K) for T, k, E, N, K in G.GROUPED for glu in (0, 1)]
