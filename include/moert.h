@@ -65,7 +65,8 @@ typedef enum {
   MOE_EUNSUPPORTED = -7  /* device lacks a needed feature                     */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP4 = 2 } moe_dtype;
+/* MOE_F8: e4m3 codes with fp32 scales; operators without a context only. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP4 = 2, MOE_F8 = 3 } moe_dtype;
 
 /* Miss handling [satyajit, "Four backends, and the one that has to be
  * measured"]: HYBRID fills q = clamp(round_half_even(m*B_P/B_H), 1, m) misses
@@ -416,8 +417,8 @@ typedef struct {
 moe_status moe_ctx_timing(moe_ctx* ctx, moe_timing* out, int32_t reset);
 
 /* ------------------------------------------------------------------------
- * Operators without a context: MXFP4 conversion and products, and the pieces
- * of a routed FFN over weights that are resident in device memory (the pages'
+ * Operators without a context: MXFP4 and F8 conversion and products, the norms
+ * around a block, and the pieces of a routed FFN over weights that are resident in device memory (the pages'
  * design keeps them in host memory; a layer that fits, a shared expert or a
  * dense projection needs none of the slot machinery).  They follow the
  * conventions above, and:
@@ -429,6 +430,10 @@ moe_status moe_ctx_timing(moe_ctx* ctx, moe_timing* out, int32_t reset);
  *   - an MXFP4 matrix is codes [rows][cols/2] and scales [rows][cols/32], both
  *     contiguous, in the bank format (OCP MX v1.0 E2M1, low nibble = even
  *     element, one E8M0 scale per 32 elements of a row; scale 255 is NaN);
+ *   - an F8 matrix is OCP e4m3 codes [rows][cols], cols a multiple of 16, and fp32
+ *     scales: one per 128 columns of a row ([rows][ceil(cols/128)], activations) or
+ *     one per 128 x 128 tile ([ceil(rows/128)][ceil(cols/128)], weights; the last
+ *     row and column of tiles may be smaller).  A value is code * scale;
  *   - rows of x and of weights are addressed in 16-byte pieces: base addresses
  *     of x, of W and of codes are 16-byte aligned, and a leading
  *     dimension (elements from one row to the next) keeps every row of x so.
@@ -466,6 +471,35 @@ moe_status moe_mx_gemm(const void* x, moe_dtype x_dtype, const uint8_t* x_scales
                        const uint8_t* w_codes, const uint8_t* w_scales, void* y, moe_dtype y_dtype,
                        int64_t ldy, int32_t M, int32_t N, int32_t K, moe_stream stream);
 
+/* F32 or BF16 to F8.  Per block of block_rows x 128 (block_rows 1 or 128):
+ * scale = max|x| / 448, at least 2^-126 (a block of zeros too); code = x * (1 /
+ * scale) to the nearest e4m3 value, ties to the even code.  Quotient, reciprocal
+ * and product are fp32 numbers, each rounded to nearest.  A block that holds an
+ * infinity or a NaN becomes NaN as a whole (scale NaN, codes 0).
+ * x: n_mats matrices (any number; with block_rows 1 exactly one) of [rows][cols], ldx elements
+ * from row to row and x_stride from matrix to matrix; codes [n_mats][rows][cols]
+ * and scales [n_mats][ceil(rows/block_rows)][ceil(cols/128)] contiguous, so that
+ * each matrix has tiles of its own.  cols % 16 == 0; x and its rows aligned to
+ * their element, codes to 16 bytes, scales to 4. */
+moe_status moe_f8_quantize(const void* x, moe_dtype x_dtype, int32_t n_mats, int64_t rows, int32_t cols,
+                           int64_t ldx, int64_t x_stride, int32_t block_rows, uint8_t* codes, float* scales,
+                           moe_stream stream);
+
+/* code * scale in fp32, as F32 or rounded to BF16.  y as x above. */
+moe_status moe_f8_dequantize(const uint8_t* codes, const float* scales, int32_t n_mats, int64_t rows,
+                             int32_t cols, int32_t block_rows, void* y, moe_dtype y_dtype, int64_t ldy,
+                             int64_t y_stride, moe_stream stream);
+
+/* y[M][N] = x[M][K] * W[N][K]^T, both F8: x with a scale per 128 columns of a
+ * row (x_scales [M][ceil(K/128)]; ldx >= K codes from row to row, a multiple of 16), W with
+ * one per 128 x 128 tile.  The codes' products of a block of K are summed in
+ * fp32, times (x scale * W scale), itself an fp32 number, and added up in fp32;
+ * one rounding to y_dtype (BF16 or F32).  K % 16 == 0, K <= 2^30, any N; ldy >= N;
+ * scales aligned to 4 bytes. */
+moe_status moe_f8_gemm(const uint8_t* x, const float* x_scales, int64_t ldx, const uint8_t* w,
+                       const float* w_scales, void* y, moe_dtype y_dtype, int64_t ldy, int32_t M, int32_t N,
+                       int32_t K, moe_stream stream);
+
 /* The T*k routed pairs (pair p = t*k + j) ordered by expert: offsets [E+1]
  * receives the first position of each expert (offsets[E] = pairs with an
  * expert in 0..E-1), perm [T*k] the pair at each position, pairs of one expert
@@ -485,8 +519,11 @@ moe_status moe_group_pairs(const int32_t* ids, int32_t T, int32_t k, int32_t E, 
  *   y[y_index ? y_index[p] : p] = row(p), or with glu = 1
  *   silu(row(p)[0..N/2)) * row(p)[N/2..N)  (N/2 columns; gate rows first, then
  *   up rows, as gate and up lie in a bank).
- * Types (x, W): (BF16, BF16), (BF16, MXFP4), (MXFP4, MXFP4); y BF16 or F32;
- * fp32 accumulation and SiLU, one rounding.  With x_index = perm, x_index_div
+ * Types (x, W): (BF16, BF16), (BF16, MXFP4), (MXFP4, MXFP4), (F8, F8); y BF16 or
+ * F32; fp32 accumulation and SiLU, one rounding.  F8: the scales are fp32 (the
+ * pointers point at floats), x_scales [n_x][ceil(K/128)], w_scales [ceil(N/128)]
+ * [ceil(K/128)] per expert; with glu gate and up are matrices of their own,
+ * 2 * ceil(N/2/128) rows of scales, the gate's first.  With x_index = perm, x_index_div
  * = k the rows of x are tokens; with y_index = perm the rows of y are pairs.
  * offsets and the indices are read on the device and never on the host:
  * positions before offsets[0] or from offsets[E] on leave y as it was; an
@@ -499,7 +536,7 @@ moe_status moe_group_pairs(const int32_t* ids, int32_t T, int32_t k, int32_t E, 
  * scales at w_scales + e * ws_stride), so a matrix inside expert banks can be
  * used in place.  w_stride is a multiple of 16 bytes and one expert's matrix
  * stays below 2^31 bytes.  K % 32 == 0 where an operand is MXFP4, else K % 8
- * == 0; K <= 2^30.  With x_index, the rows of x span less than 2^31 bytes. */
+ * == 0 (F8: 16); K <= 2^30.  With x_index, the rows of x span less than 2^31 bytes. */
 typedef struct {
   int32_t n_experts;         /* E (1..1024)                                       */
   int32_t n_rows;            /* positions, >= 0                                   */
@@ -507,13 +544,13 @@ typedef struct {
   int32_t x_dtype, w_dtype, y_dtype; /* moe_dtype                                 */
   int32_t glu;               /* 0 or 1 (N even)                                   */
   const void* x;             /* [n_x][K], ldx elements from row to row (MXFP4: K) */
-  const uint8_t* x_scales;   /* MXFP4 x: [n_x][K/32], else NULL                   */
+  const uint8_t* x_scales;   /* MXFP4 x: [n_x][K/32]; F8: fp32; else NULL         */
   int64_t ldx;
   int32_t n_x;               /* rows of x, >= 1; >= n_rows without x_index         */
   int32_t x_index_div;       /* >= 1                                              */
   const int32_t* x_index;    /* [n_rows] or NULL                                  */
   const void* w;
-  const uint8_t* w_scales;   /* MXFP4 weights, else NULL                          */
+  const uint8_t* w_scales;   /* MXFP4 and F8 (fp32) weights, else NULL            */
   int64_t w_stride, ws_stride; /* bytes from expert to expert                     */
   const int32_t* offsets;    /* [E+1]                                             */
   void* y;                   /* [n_y][N or N/2], ldy elements from row to row     */
@@ -535,6 +572,53 @@ moe_status moe_grouped_gemm(const moe_grouped_args* args, moe_stream stream);
 moe_status moe_combine_pairs(const void* p, moe_dtype p_dtype, int64_t ldp, const float* w,
                              const int32_t* ids, int32_t E, int32_t T, int32_t k, int32_t H, void* y,
                              moe_dtype y_dtype, int64_t ldy, moe_stream stream);
+
+/* The norm in front of a block:
+ *   y[t] = x[t] / sqrt(mean(x[t]^2) + eps) * weight
+ * in fp32, rounded once.  x [T][H] F32 or BF16, ldx elements from row to row;
+ * weight [H] F32 or BF16; y F32, BF16 (y_scales NULL) or F8 with y_scales
+ * [T][ceil(H/128)], converted from the fp32 values as moe_f8_quantize does, ldy
+ * elements from row to row.  H in 1..32768 (F8: a multiple of 16, y and its rows
+ * 16-byte aligned); eps a positive normal number.  Any finite row is
+ * normed, also where its squares leave fp32.  Alignment: that of the elements. */
+moe_status moe_norm(const void* x, moe_dtype x_dtype, int64_t ldx, const void* weight, moe_dtype weight_dtype,
+                    float eps, int64_t T, int32_t H, void* y, moe_dtype y_dtype, float* y_scales, int64_t ldy,
+                    moe_stream stream);
+
+/* The end of a block and the norm in front of the next one:
+ *   b[t]   = sum over ascending j of w[t][j] * p[t*k + j]     (moe_combine_pairs' sum)
+ *   n[t]   = post_weight ? b[t] / sqrt(mean(b[t]^2) + eps) * post_weight : b[t]
+ *   r[t]   = residual[t] + scale * gate[t] * n[t]
+ *   out[t] = r[t]
+ *   y[t]   = r[t] / sqrt(mean(r[t]^2) + eps) * weight          (with weight)
+ * in fp32 throughout: y comes from r before its rounding to out's type.  w NULL:
+ * k = 1 and the block's rows are p themselves (a dense or attention block).
+ * ids [T][k] or NULL: pairs with an id outside 0..E-1 are left out and their rows
+ * are not read; a token without any keeps its residual.  gate: F32 or BF16, ldg elements
+ * from row to row (0: one row for all tokens), gate_cols H (a value per channel)
+ * or 1 (per token), or NULL.  out may be residual itself (same type and ldout =
+ * ldres), else they must not overlap.  y, y_scales as in moe_norm, NULL without
+ * weight. */
+typedef struct {
+  const void* p;             /* [T*k][H], ldp elements from row to row            */
+  const float* w;            /* [T][k] or NULL                                    */
+  const int32_t* ids;        /* [T][k] or NULL                                    */
+  const void* residual;      /* [T][H], ldres                                     */
+  void* out;                 /* [T][H], ldout                                     */
+  const void* post_weight;   /* [H] or NULL                                       */
+  const void* gate;          /* or NULL                                           */
+  const void* weight;        /* [H] or NULL                                       */
+  void* y;                   /* [T][H], ldy                                       */
+  float* y_scales;           /* [T][ceil(H/128)] with F8 y, else NULL             */
+  int64_t ldp, ldres, ldout, ldg, ldy;
+  int64_t T;
+  int32_t k, H, n_experts, gate_cols;
+  int32_t p_dtype, residual_dtype, out_dtype, post_dtype, gate_dtype, weight_dtype, y_dtype; /* moe_dtype */
+  int32_t reserved;          /* 0                                                 */
+  float scale, eps;
+} moe_combine_norm_args;
+
+moe_status moe_combine_norm(const moe_combine_norm_args* args, moe_stream stream);
 
 const char* moe_strerror(moe_status s);
 /* Text of the last error on the calling thread ("" if none). */

@@ -91,3 +91,66 @@ def combine(p, w, ids=None, E=0):
         w = np.where(ok, w, 0.0)
     t = w[:, :, None] * p
     return t.sum(1), np.abs(t).sum(1)
+
+
+# ------------------------------------------------------------------ F8 and norms
+def _e4m3_table() -> np.ndarray:
+    """The value of each OCP e4m3 code: 4 exponent bits (bias 7), 3 of mantissa, no infinities, S.1111.111 NaN."""
+    c = np.arange(256)
+    e, m = (c >> 3) & 15, c & 7
+    v = np.where(e == 0, m * 2.0 ** -9, (1 + m / 8) * np.exp2(e - 7.0))
+    v = np.where((c & 127) == 127, np.nan, v)
+    return np.where(c >= 128, -v, v)
+
+
+E4M3 = _e4m3_table()
+
+
+def f8_codes(q: np.ndarray) -> np.ndarray:
+    """The code nearest to each q, |q| < 464; of two equally near ones the even code."""
+    mags = E4M3[:127]
+    a = np.abs(q)
+    hi = np.clip(np.searchsorted(mags, a), 1, 126)
+    lo = hi - 1
+    up, down = mags[hi] - a, a - mags[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    return np.where(np.signbit(q), code | 128, code).astype(np.uint8)
+
+
+def f8_quantize(x: np.ndarray, block_rows: int = 1):
+    """x [R, C] (exact in fp64) -> (codes uint8 [R, C], scales f32).  Scale, reciprocal and product are fp32 numbers."""
+    x = np.asarray(x, np.float64)
+    R, C = x.shape
+    rb, cb = -(-R // block_rows), -(-C // 128)
+    codes, scales = np.zeros((R, C), np.uint8), np.zeros((rb, cb), np.float32)
+    for j in range(cb):
+        part = x[:, j * 128:(j + 1) * 128]
+        rows = np.zeros((rb * block_rows, part.shape[1]))
+        rows[:R] = part
+        v = rows.reshape(rb, -1)
+        bad = ~np.isfinite(v).all(axis=1)
+        v = np.where(bad[:, None], 0.0, v)
+        s = np.maximum((np.abs(v).max(axis=1) / 448).astype(np.float32), np.float32(2.0 ** -126))
+        inv = (1.0 / s.astype(np.float64)).astype(np.float32).astype(np.float64)
+        with np.errstate(under="ignore"):
+            q = (v * inv[:, None]).astype(np.float32).astype(np.float64)
+        codes[:, j * 128:(j + 1) * 128] = f8_codes(q).reshape(rb * block_rows, -1)[:R]
+        codes[np.repeat(bad, block_rows)[:R], j * 128:(j + 1) * 128] = 0
+        scales[:, j] = np.where(bad, np.float32(np.nan), s)
+    return codes, scales
+
+
+def f8_values(codes: np.ndarray, scales: np.ndarray, block_rows: int = 1) -> np.ndarray:
+    R, C = codes.shape
+    s = np.repeat(np.asarray(scales, np.float64), 128, axis=1)[:, :C]
+    s = np.repeat(s, block_rows, axis=0)[:R]
+    with np.errstate(invalid="ignore"):
+        return E4M3[codes] * s
+
+
+def norm(x, weight, eps):
+    """(y, inverse root of each row)."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(all="ignore"):
+        inv = 1 / np.sqrt((x * x).mean(axis=1, keepdims=True) + eps)
+        return x * inv * np.asarray(weight, np.float64), inv

@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libmoert.so")
 
 MOE_OK, MOE_EINVAL, MOE_ENOMEM, MOE_ENOSPC, MOE_EHIP, MOE_EBUSY, MOE_ETIMEDOUT, \
     MOE_EUNSUPPORTED = 0, -1, -2, -3, -4, -5, -6, -7
-MOE_F32, MOE_BF16, MOE_MXFP4 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_MXFP4, MOE_F8 = 0, 1, 2, 3
 MOE_HYBRID, MOE_OFFLOAD, MOE_CPU = 0, 1, 2
 DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp4": MOE_MXFP4}
 
@@ -92,6 +92,16 @@ class GroupedArgs(ctypes.Structure):
                 ("y_index", ctypes.c_void_p)]
 
 
+class CombineNormArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("p", "w", "ids", "residual", "out", "post_weight", "gate", "weight", "y", "y_scales")] + \
+               [(n, ctypes.c_int64) for n in ("ldp", "ldres", "ldout", "ldg", "ldy", "T")] + \
+               [(n, ctypes.c_int32) for n in
+                ("k", "H", "n_experts", "gate_cols", "p_dtype", "residual_dtype", "out_dtype", "post_dtype",
+                 "gate_dtype", "weight_dtype", "y_dtype", "reserved")] + \
+               [("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 class MoertError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         self.status = status
@@ -111,6 +121,7 @@ def lib():
                 "(python -m routed_expert_execution_moe_amd.build or __graft_entry__.build())")
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        f32 = ctypes.c_float
         cfgp = ctypes.POINTER(MoeConfig)
         sig = {
             "moe_expert_bytes": ([cfgp], sz),
@@ -138,6 +149,11 @@ def lib():
             "moe_mx_quantize": ([vp, i32, i64, i32, i64, vp, vp, vp], i32),
             "moe_mx_dequantize": ([vp, vp, i64, i32, vp, i32, i64, vp], i32),
             "moe_mx_gemm": ([vp, i32, vp, i64, vp, vp, vp, i32, i64, i32, i32, i32, vp], i32),
+            "moe_f8_quantize": ([vp, i32, i32, i64, i32, i64, i64, i32, vp, vp, vp], i32),
+            "moe_f8_dequantize": ([vp, vp, i32, i64, i32, i32, vp, i32, i64, i64, vp], i32),
+            "moe_f8_gemm": ([vp, vp, i64, vp, vp, vp, i32, i64, i32, i32, i32, vp], i32),
+            "moe_norm": ([vp, i32, i64, vp, i32, f32, i64, i32, vp, i32, vp, i64, vp], i32),
+            "moe_combine_norm": ([ctypes.POINTER(CombineNormArgs), vp], i32),
             "moe_group_workspace": ([i32, i32, i32], sz),
             "moe_group_pairs": ([vp, i32, i32, i32, vp, vp, vp, sz, vp], i32),
             "moe_grouped_gemm": ([ctypes.POINTER(GroupedArgs), vp], i32),
@@ -315,6 +331,8 @@ def moe_ctx_timing(ctx, reset=False) -> dict:
 # caller's to order and to keep (torch.Tensor.record_stream), as with any kernel.
 _FLOATS = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _U8, _I32, _BF16, _F32 = (torch.uint8,), (torch.int32,), (torch.bfloat16,), (torch.float32,)
+_F8 = (torch.float8_e4m3fn,)
+_ROWS = {**_FLOATS, torch.float8_e4m3fn: MOE_F8}
 _INT = 1 << 31
 
 
@@ -400,6 +418,11 @@ def moe_mx_dequantize(codes, scales, y, stream=None):
 
 def _rows_operand(me, x, x_scales):
     """(rows, K, dtype, ldx) of x: bf16 rows, or codes with their scales."""
+    if x.__class__ is torch.Tensor and x.dtype is torch.float8_e4m3fn:
+        R, K, ld = _matrix(me, "x", x, _F8)
+        _need(x_scales is not None, me, "x in 8 bits needs x_scales")
+        _whole(me, "x_scales", x_scales, _F32, (R, -(-K // 128)))
+        return R, K, MOE_F8, ld
     if x_scales is None:
         R, K, ld = _matrix(me, "x", x, _BF16)
         return R, K, MOE_BF16, ld
@@ -427,6 +450,64 @@ def moe_mx_gemm(x, w_codes, w_scales, y, x_scales=None, stream=None):
           K)
 
 
+def _f8_operand(me, v, codes, scales, block_rows, name):
+    """Checks one F8 conversion; (matrices, rows, columns, elements from row to row, from matrix to matrix) of v."""
+    _need(block_rows in (1, 128), me, "block_rows must be 1 or 128")
+    n, stride = 1, 0
+    if block_rows == 128 and isinstance(v, torch.Tensor) and v.dim() == 3:
+        if not (v.is_contiguous() and v.dtype in _FLOATS):
+            _check_tensor(me, name, v, 3, _FLOATS)
+        n, R, C = v.shape
+        ld, stride = v.stride(1) if R > 1 else C, v.stride(0) if n > 1 else 0
+        _need(n < _INT and R < _INT and C < _INT, me, f"{name} is too large")
+    else:
+        R, C, ld = _matrix(me, name, v, _FLOATS)
+    rows = R if block_rows == 1 else -(-R // 128)
+    _need(C % 16 == 0, me, "the columns must be a multiple of 16")
+    lead = v.shape[:-2]
+    _whole(me, "codes", codes, _F8, (*lead, R, C))
+    _whole(me, "scales", scales, _F32, (*lead, rows, -(-C // 128)))
+    return n, R, C, ld, stride
+
+
+def moe_f8_quantize(x, codes, scales, block_rows=1, stream=None):
+    """x [R, C] f32 or bf16 (rows may be strided) -> codes float8_e4m3fn [R, C],
+    scales f32 [R, ceil(C/128)]; with block_rows=128 one scale per 128 x 128
+    tile, [ceil(R/128), ceil(C/128)], and x may be [n, R, C] (codes and scales
+    then too).  No gradient."""
+    me = "moe_f8_quantize"
+    n, R, C, ld, stride = _f8_operand(me, x, codes, scales, block_rows, "x")
+    _call(me, lib().moe_f8_quantize, (x, codes, scales), stream, x.data_ptr(), _FLOATS[x.dtype], n, R, C, ld, stride,
+          block_rows, codes.data_ptr(), scales.data_ptr())
+
+
+def moe_f8_dequantize(codes, scales, y, block_rows=1, stream=None):
+    """codes and scales as moe_f8_quantize leaves them -> y f32 or bf16 of the
+    codes' shape (rows may be strided).  No gradient."""
+    me = "moe_f8_dequantize"
+    n, R, C, ld, stride = _f8_operand(me, y, codes, scales, block_rows, "y")
+    _call(me, lib().moe_f8_dequantize, (y, codes, scales), stream, codes.data_ptr(), scales.data_ptr(), n, R, C,
+          block_rows, y.data_ptr(), _FLOATS[y.dtype], ld, stride)
+
+
+def moe_f8_gemm(x, x_scales, w, w_scales, y, stream=None):
+    """y [M, N] (f32 or bf16) = x W^T; x float8_e4m3fn [M, K] (rows may be strided)
+    with x_scales f32 [M, ceil(K/128)], W float8_e4m3fn [N, K] with w_scales f32
+    [ceil(N/128), ceil(K/128)].  No gradient."""
+    me = "moe_f8_gemm"
+    M, K, ldx = _matrix(me, "x", x, _F8)
+    KB = -(-K // 128)
+    _whole(me, "x_scales", x_scales, _F32, (M, KB))
+    N, C, _ = _matrix(me, "w", w, _F8)
+    _whole(me, "w", w, _F8, (N, K))
+    _whole(me, "w_scales", w_scales, _F32, (-(-N // 128), KB))
+    Y, C, ldy = _matrix(me, "y", y, _FLOATS)
+    if Y != M or C != N:
+        _need(False, me, f"y: shape {(Y, C)}, expected {(M, N)}")
+    _call(me, lib().moe_f8_gemm, (x, x_scales, w, w_scales, y), stream, x.data_ptr(), x_scales.data_ptr(), ldx,
+          w.data_ptr(), w_scales.data_ptr(), y.data_ptr(), _FLOATS[y.dtype], ldy, M, N, K)
+
+
 def moe_group_workspace(T, k, E):
     return lib().moe_group_workspace(T, k, E)
 
@@ -451,19 +532,30 @@ def moe_grouped_gemm(x, w, offsets, y, x_scales=None, w_scales=None, x_index=Non
                      y_index=None, glu=False, stream=None):
     """Row p of the positions offsets[e] <= p < offsets[e+1] times expert e's W^T.
     x bf16 [n_x, K] or codes [n_x, K/2] with x_scales; w bf16 [E, N, K] or codes
-    [E, N, K/2] with w_scales [E, N, K/32] (any stride from expert to expert);
-    y [n_y, N], or [n_y, N/2] with glu; x_index, y_index int32 [n_rows].  The
+    [E, N, K/2] with w_scales [E, N, K/32] (any stride from expert to expert); or
+    both float8_e4m3fn, x [n_x, K] with x_scales f32 [n_x, ceil(K/128)], w [E, N, K]
+    with w_scales f32 [E, ceil(N/128), ceil(K/128)] (with glu [E, 2*ceil(N/2/128),
+    ceil(K/128)]: gate and up are matrices of their own); y [n_y, N], or [n_y, N/2] with glu; x_index, y_index int32 [n_rows].  The
     positions are those of an index, else the rows of x.  No gradient."""
     me = "moe_grouped_gemm"
     n_x, K, x_dtype, ldx = _rows_operand(me, x, x_scales)
-    row, dtypes = (K, _BF16) if w_scales is None else (K // 2, _U8)
+    f8 = x_dtype == MOE_F8
+    row, dtypes = (K, _F8) if f8 else (K, _BF16) if w_scales is None else (K // 2, _U8)
     if not (w.__class__ is torch.Tensor and w.is_contiguous() and w.dtype in dtypes and len(w.shape) == 3
             and w.shape[2] == row and max(w.shape) < _INT):
         _check_tensor(me, "w", w, 3, dtypes, (None, None, row))
         _need(w.shape[1] == 1 or w.stride(1) == row, me, "w: rows of one expert must be contiguous")
     E, N = w.shape[:2]
     ws_ptr, ws_stride = None, 0
-    if w_scales is not None:
+    if f8:
+        shape = (E, 2 * -(-(N // 2) // 128) if glu else -(-N // 128), -(-K // 128))
+        if not (w_scales.__class__ is torch.Tensor and w_scales.is_contiguous() and w_scales.dtype in _F32
+                and w_scales.shape == shape):
+            _check_tensor(me, "w_scales", w_scales, 3, _F32, shape)
+            _need(shape[1] == 1 or w_scales.stride(1) == shape[2], me, "w_scales: rows of one expert must be contiguous")
+        ws_ptr = w_scales.data_ptr()
+        ws_stride = w_scales.stride(0) * 4 if E > 1 else 0
+    elif w_scales is not None:
         _need(K % 32 == 0, me, "K must be a multiple of 32")
         if not (w_scales.__class__ is torch.Tensor and w_scales.is_contiguous() and w_scales.dtype in _U8
                 and w_scales.shape == (E, N, K // 32)):
@@ -483,7 +575,7 @@ def moe_grouped_gemm(x, w, offsets, y, x_scales=None, w_scales=None, x_index=Non
     n_y, cols, ldy = _matrix(me, "y", y, _FLOATS)
     if cols != (N // 2 if glu else N):
         _need(False, me, f"y has {cols} columns, expected {N // 2 if glu else N}")
-    a = GroupedArgs(E, n_rows, N, K, x_dtype, MOE_BF16 if w_scales is None else MOE_MXFP4, _FLOATS[y.dtype],
+    a = GroupedArgs(E, n_rows, N, K, x_dtype, MOE_F8 if f8 else MOE_BF16 if w_scales is None else MOE_MXFP4, _FLOATS[y.dtype],
                     1 if glu else 0, x.data_ptr(), _ptr(x_scales), ldx, n_x, x_index_div, _ptr(x_index),
                     w.data_ptr(), ws_ptr, w.stride(0) * w.element_size() if E > 1 else 0, ws_stride,
                     offsets.data_ptr(), y.data_ptr(), ldy, n_y, 0, _ptr(y_index))
@@ -508,6 +600,82 @@ def moe_combine_pairs(p, w, y, ids=None, n_experts=0, stream=None):
         n_experts = 0
     _call(me, lib().moe_combine_pairs, (p, w, y, ids), stream, p.data_ptr(), _FLOATS[p.dtype], ldp, w.data_ptr(),
           _ptr(ids), n_experts, T, k, H, y.data_ptr(), _FLOATS[y.dtype], ldy)
+
+
+def _norm_output(me, y, y_scales, T, H):
+    """(dtype, elements from row to row) of rows that leave a norm."""
+    Y, C, ldy = _matrix(me, "y", y, _ROWS)
+    if Y != T or C != H:
+        _need(False, me, f"y: shape {(Y, C)}, expected {(T, H)}")
+    if y.dtype is torch.float8_e4m3fn:
+        _need(y_scales is not None, me, "y in 8 bits needs y_scales")
+        _whole(me, "y_scales", y_scales, _F32, (T, -(-H // 128)))
+    else:
+        _need(y_scales is None, me, "y_scales belong to a y in 8 bits")
+    return _ROWS[y.dtype], ldy
+
+
+def moe_norm(x, weight, y, y_scales=None, eps=1e-6, stream=None):
+    """y [T, H] = x / sqrt(mean(x^2) + eps) * weight; x f32 or bf16 [T, H], weight
+    f32 or bf16 [H]; y f32, bf16, or float8_e4m3fn with y_scales f32 [T,
+    ceil(H/128)].  Rows of x and y may be strided.  No gradient."""
+    me = "moe_norm"
+    T, H, ldx = _matrix(me, "x", x, _FLOATS)
+    _whole(me, "weight", weight, _FLOATS, (H,))
+    y_dtype, ldy = _norm_output(me, y, y_scales, T, H)
+    _call(me, lib().moe_norm, (x, weight, y, y_scales), stream, x.data_ptr(), _FLOATS[x.dtype], ldx, weight.data_ptr(),
+          _FLOATS[weight.dtype], eps, T, H, y.data_ptr(), y_dtype, _ptr(y_scales), ldy)
+
+
+def moe_combine_norm(p, w, residual, out, ids=None, n_experts=0, post_weight=None, gate=None, scale=1.0, weight=None,
+                     y=None, y_scales=None, eps=1e-6, stream=None):
+    """The end of a block and the next block's norm, in fp32:
+        b = sum over j of w[t, j] * p[t*k + j]       (w None: b = p)
+        n = b / sqrt(mean(b^2) + eps) * post_weight  (post_weight None: n = b)
+        out = r = residual + scale * gate * n
+        y = r / sqrt(mean(r^2) + eps) * weight       (weight and y None: not made)
+    p [T*k, H], residual and out [T, H] (out may be residual), gate [T or 1, H
+    or 1], all f32 or bf16 with rows that may be strided; w f32 [T, k];
+    post_weight, weight f32 or bf16 [H]; with ids int32 [T, k], pairs outside
+    0..n_experts-1 are left out; y and y_scales as in moe_norm.  No gradient."""
+    me = "moe_combine_norm"
+    T, H, ldres = _matrix(me, "residual", residual, _FLOATS)
+    R, C, ldp = _matrix(me, "p", p, _FLOATS)
+    k = 1
+    if w is not None:
+        W, k, ld = _matrix(me, "w", w, _F32)
+        _need(W == T and (T < 2 or ld == k), me, "w must be contiguous, with a row per token")
+    if R != T * k or C != H:
+        _need(False, me, f"residual {(T, H)}, {k} rows a token and p {(R, C)} do not belong together")
+    O, C, ldout = _matrix(me, "out", out, _FLOATS)
+    if O != T or C != H:
+        _need(False, me, f"out: shape {(O, C)}, expected {(T, H)}")
+    if ids is not None:
+        _whole(me, "ids", ids, _I32, (T, k))
+        _need(0 < n_experts < _INT, me, "ids need n_experts >= 1")
+    else:
+        n_experts = 0
+    if post_weight is not None:
+        _whole(me, "post_weight", post_weight, _FLOATS, (H,))
+    ldg = gate_cols = 0
+    if gate is not None:
+        G, gate_cols, _ = _matrix(me, "gate", gate, _FLOATS)
+        _need(G in (1, T) and gate_cols in (1, H), me, f"gate: shape {(G, gate_cols)}, expected [1 or {T}, 1 or {H}]")
+        ldg = gate.stride(0) if G > 1 else 0
+    y_dtype = ldy = 0
+    _need((weight is None) == (y is None), me, "weight and y belong together")
+    if weight is not None:
+        _whole(me, "weight", weight, _FLOATS, (H,))
+        y_dtype, ldy = _norm_output(me, y, y_scales, T, H)
+    else:
+        _need(y_scales is None, me, "y_scales belong to a y in 8 bits")
+    a = CombineNormArgs(p.data_ptr(), _ptr(w), _ptr(ids), residual.data_ptr(), out.data_ptr(), _ptr(post_weight),
+                        _ptr(gate), _ptr(weight), _ptr(y), _ptr(y_scales), ldp, ldres, ldout, ldg, ldy, T, k, H,
+                        n_experts, gate_cols, _FLOATS[p.dtype], _FLOATS[residual.dtype], _FLOATS[out.dtype],
+                        0 if post_weight is None else _FLOATS[post_weight.dtype], 0 if gate is None else _FLOATS[gate.dtype],
+                        0 if weight is None else _FLOATS[weight.dtype], y_dtype, 0, scale, eps)
+    _call(me, lib().moe_combine_norm, (residual, p, out, w, ids, post_weight, gate, weight, y, y_scales), stream,
+          ctypes.byref(a))
 
 
 def moe_strerror(status: int) -> str:

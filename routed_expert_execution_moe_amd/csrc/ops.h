@@ -27,10 +27,10 @@ inline hipError_t launch_op(void (*f)(P...), dim3 grid, dim3 block, hipStream_t 
 // Operands of y = x W^T, grouped by expert; a dense product is one group
 // (offsets == nullptr) of n_rows rows.
 struct ProductArgs {
-  const uint8_t* x;         // rows of bf16 or of MXFP4 codes
-  const uint8_t* xs;        // [n_x][K/32] scales of MXFP4 rows
+  const uint8_t* x;         // rows of bf16 or of MXFP4 or F8 codes
+  const uint8_t* xs;        // [n_x][K/32] scales of MXFP4 rows; F8: fp32 [n_x][ceil(K/128)]
   const uint8_t* w;         // expert e at w + e * w_stride, [N][K]
-  const uint8_t* ws;        // [N][K/32] at ws + e * ws_stride
+  const uint8_t* ws;        // [N][K/32] at ws + e * ws_stride; F8: fp32, one per 128 x 128 tile
   int64_t x_ld;             // bytes from row to row of x
   int64_t w_stride, ws_stride;
   const int32_t* x_index;   // [n_rows] or nullptr
@@ -45,6 +45,34 @@ hipError_t launch_mx_quantize(const void* x, bool f32, int64_t rows, int cols, i
                               uint8_t* scales, hipStream_t s);
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int cols,
                                 void* y, bool f32, int64_t ldy, hipStream_t s);
+// n_mats matrices of [rows][cols]; ldx and stride in elements
+hipError_t launch_f8_quantize(const void* x, bool f32, int n_mats, int64_t rows, int cols, int64_t ldx,
+                              int64_t stride, bool tiles, uint8_t* codes, float* scales, hipStream_t s);
+hipError_t launch_f8_dequantize(const uint8_t* codes, const float* scales, int n_mats, int64_t rows, int cols,
+                                bool tiles, void* y, bool f32, int64_t ldy, int64_t stride, hipStream_t s);
+
+// The norm in front of a block (p = x, no residual) or the end of one; dimensions
+// and strides in elements.
+struct NormArgs {
+  const uint8_t* p;
+  const float* w;
+  const int32_t* ids;
+  const uint8_t* res;
+  uint8_t* out;
+  const uint8_t* post;
+  const uint8_t* gate;
+  const uint8_t* weight;
+  uint8_t* y;
+  float* ys;
+  int64_t ldp, ldres, ldout, ldg, ldy, T;
+  int k, H, E, gate_cols;
+  int p_f32, res_f32, out_f32, post_f32, gate_f32, weight_f32;
+  int y_dtype;
+  int lg;  // log2 of the threads per row, or 10 and more for a whole workgroup
+  float scale, eps;
+};
+hipError_t launch_norm(NormArgs a, hipStream_t s);
+
 // x_dtype / w_dtype as in moe_grouped_gemm; hipErrorInvalidConfiguration when
 // the product needs more workgroups than a launch may have
 hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool glu, hipStream_t s);
@@ -96,6 +124,15 @@ __device__ inline op_bf16x8 op_fp4x8(uint32_t raw, float scale) {
   return op_bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
+// 8 e4m3 codes, first in the lowest byte, as bf16 (exact)
+__device__ inline op_bf16x8 op_f8x8_values(uint32_t lo, uint32_t hi) {
+  const op_bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
+  const op_bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
+  const op_bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
+  const op_bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+  return op_bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
 // silu(g) * u.  With h = exp(-|g| / 2) the sigmoid is 1 / (1 + h^2), for g < 0
 // times h^2: nothing overflows, and the reciprocal (1 ulp, a fraction of a correct
 // division's instructions) is of 1..2, so it is no subnormal that the
@@ -110,6 +147,112 @@ __device__ inline float op_silu_mul(float g, float u) {
   const float s = g * __builtin_amdgcn_rcpf(fmaf(h, h, 1.f));
   const float f = g < 0.f ? h : 1.f;
   return s * f * u * f;
+}
+
+// the largest of 16 lanes' values (a DPP row), in each of them
+__device__ inline uint32_t op_max16(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));   // lane ^ 1
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // lane ^ 2
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // mirrored in 8
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // mirrored in 16
+  return v;
+}
+
+// F8 scale of a block and its reciprocal, from the bits of the largest magnitude
+// (their order as integers is that of the magnitudes; infinities and NaN come out
+// on top and make the block NaN, with codes of 0 from the reciprocal's flag)
+struct OpF8Scale {
+  float scale, inv;
+  bool bad;
+  __device__ inline explicit OpF8Scale(uint32_t top) {
+    bad = top >= 0x7F800000u;
+    const float s = fmaxf(__uint_as_float(bad ? 0 : top) / 448.f, 0x1p-126f);
+    scale = bad ? __uint_as_float(0x7FC00000u) : s;
+    inv = 1.f / s;
+  }
+};
+
+// 8 e4m3 codes of v * inv, first in the lowest byte.  |v * inv| is below 448.0001, so
+// nothing saturates.
+__device__ inline uint2 op_f8x8(const float (&v)[8], const OpF8Scale& s) {
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * s.inv, v[1] * s.inv, lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * s.inv, v[3] * s.inv, lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * s.inv, v[5] * s.inv, hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * s.inv, v[7] * s.inv, hi, true);
+  return s.bad ? make_uint2(0, 0) : make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+// 16 bytes at an address of any alignment: global memory takes them in one access
+typedef unsigned int op_bytes16 __attribute__((ext_vector_type(4), aligned(1)));
+
+// 8 columns of a row in fp32 or bf16, as loaded
+struct OpCols {
+  op_u32x4 a, b;
+};
+__device__ inline OpCols op_cols_load(const uint8_t* row, bool f32, int64_t c) {
+  OpCols v{};
+  const uint8_t* p = row + c * (f32 ? 4 : 2);
+  v.a = *(const op_bytes16*)p;
+  if (f32) v.b = *(const op_bytes16*)(p + 16);
+  return v;
+}
+// the first n of them (0 and fewer: none), the others zero
+__device__ inline OpCols op_cols_load(const uint8_t* row, bool f32, int64_t c, int n) {
+  if (n >= 8) return op_cols_load(row, f32, c);
+  OpCols v{};
+  if (f32) {
+    const float* p = (const float*)row + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < n) v.a[i] = __float_as_uint(p[i]);
+      if (i + 4 < n) v.b[i] = __float_as_uint(p[i + 4]);
+    }
+  } else {
+    const uint16_t* p = (const uint16_t*)row + c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) v.a[i / 2] |= (uint32_t)p[i] << (i % 2 * 16);
+  }
+  return v;
+}
+__device__ inline void op_cols_get(const OpCols& c, bool f32, float (&v)[8]) {
+  if (f32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(c.a[i]);
+      v[4 + i] = __uint_as_float(c.b[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(c.a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(c.a[i] & 0xFFFF0000u);
+    }
+  }
+}
+// the first n columns of a row at c
+__device__ inline void op_cols_store(uint8_t* row, bool f32, int64_t c, int n, const float (&v)[8]) {
+  if (f32) {
+    float* p = (float*)row + c;
+    if (n >= 8) {
+      *(op_bytes16*)p = op_u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+      *(op_bytes16*)(p + 4) = op_u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = v[i];
+    }
+  } else {
+    uint16_t* p = (uint16_t*)row + c;
+    if (n >= 8) {
+      *(op_bytes16*)p = op_u32x4{op_bf16_pair(v[0], v[1]), op_bf16_pair(v[2], v[3]), op_bf16_pair(v[4], v[5]), op_bf16_pair(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = op_bf16(v[i]);
+    }
+  }
 }
 
 struct OpTile {
@@ -192,6 +335,13 @@ struct OpTiles {
 inline int64_t op_max_tiles(const ProductArgs& a, int bm) {
   if (a.n_experts == 1) return (a.n_rows + bm - 1) / bm;
   return a.n_rows / bm + std::min(a.n_experts, a.n_rows);
+}
+
+// blocks of K with a scale of their own, and the row of W's F8 scales that holds
+// column n of part (0: all of W or the gate, 1: up)
+__host__ __device__ inline int op_f8_blocks(int K) { return (K + 127) >> 7; }
+__device__ inline int op_f8_w_block(const ProductArgs& a, bool glu, int n, int part) {
+  return (n >> 7) + (glu && part ? (a.N / 2 + 127) >> 7 : 0);
 }
 
 // Row of x that position p reads, -1 for none (the product is a row of zeros).

@@ -1,4 +1,4 @@
-// Products y = x W^T with bf16 or MXFP4 operands, dense or ragged by expert:
+// Products y = x W^T with bf16, MXFP4 or F8 operands, dense or ragged by expert:
 // the variant for few rows, and the choice between the variants.
 //
 // A workgroup of eight waves owns 16*NB rows of W (with GLU: as many gate rows
@@ -17,6 +17,11 @@
 //   bf16 x MXFP4    slice s, lane group g: k = 32g + 8s + [0,8): a lane's codes
 //                   are one 16-byte piece under one scale
 //   MXFP4 x MXFP4   lane group g: k = 32g + [0,32), the scaled MFMA's own order
+//   F8 x F8         piece c (0..1), lane group g: k = 64c + 16g + [0,16); a turn is
+//                   one scale block, whose products are summed from zero and
+//                   join the row's sum times both scales.  The codes are expanded
+//                   to bf16, which is exact: the 8-bit matrix instructions keep
+//                   13 bits of each product, and loads bound here
 //
 // One token against 4096 x 4096 in MXFP4 (8.9 MB) takes 5.6 us of kernel and
 // eight tokens of the same 7.6; 64 x 4096 x 4096 takes 15.2 us in 32 x 32 blocks.
@@ -39,8 +44,8 @@ constexpr int kSmTurn = 128;  // elements of K per wave and turn
 template <int AT, int WT, bool GLU, int MI, int NB>
 __global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(ProductArgs a) {
   constexpr int NW = GLU ? 2 * NB : NB;  // W blocks: gate blocks, then up blocks
-  constexpr bool XM = AT == MOE_MXFP4, WM = WT == MOE_MXFP4;
-  constexpr int CW = WM ? 1 : 4, CX = XM ? 1 : 4;  // 16-byte pieces per row and turn
+  constexpr bool XM = AT == MOE_MXFP4, WM = WT == MOE_MXFP4, F8 = AT == MOE_F8;
+  constexpr int CW = F8 ? 2 : WM ? 1 : 4, CX = F8 ? 2 : XM ? 1 : 4;  // 16-byte pieces per row and turn
   __shared__ op_f32x4 s_red[kSmWaves / 2][MI * NW][64];
   const int n_out = GLU ? a.N / 2 : a.N;
   const int n_blocks = (n_out + 16 * NB - 1) / (16 * NB);
@@ -59,8 +64,10 @@ __global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(Product
 #pragma unroll
   for (int b = 0; b < NW; ++b) {
     const int64_t n = min(n0 + (b % NB) * 16 + r, n_out - 1) + (b / NB) * n_out;
-    w[b] = a.w + (int64_t)t.e * a.w_stride + n * (WM ? K / 2 : K * 2);
-    ws[b] = WM ? a.ws + (int64_t)t.e * a.ws_stride + n * (K / 32) : nullptr;
+    w[b] = a.w + (int64_t)t.e * a.w_stride + n * (F8 ? K : WM ? K / 2 : K * 2);
+    ws[b] = F8   ? a.ws + (int64_t)t.e * a.ws_stride + (int64_t)op_f8_w_block(a, GLU, min(n0 + (b % NB) * 16, n_out - 1), b / NB) * op_f8_blocks(K) * 4
+            : WM ? a.ws + (int64_t)t.e * a.ws_stride + n * (K / 32)
+                 : nullptr;
   }
   const uint8_t* x[MI];
   const uint8_t* xs[MI];
@@ -71,7 +78,7 @@ __global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(Product
     const int row = m < t.rows ? op_x_row(a, t.pos0 + m) : -1;
     live[i] = row >= 0;
     x[i] = a.x + (int64_t)max(row, 0) * a.x_ld;
-    xs[i] = XM ? a.xs + (int64_t)max(row, 0) * (K / 32) : nullptr;
+    xs[i] = F8 ? a.xs + (int64_t)max(row, 0) * op_f8_blocks(K) * 4 : XM ? a.xs + (int64_t)max(row, 0) * (K / 32) : nullptr;
   }
 
   op_f32x4 acc[MI][NW];
@@ -85,7 +92,10 @@ __global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(Product
     uint32_t ws[NW], xs[MI];
   };
   // a lane's element of piece c in the turn at k0
-  auto at = [&](int k0, int c, bool codes) { return k0 + (codes ? 32 * g : WM ? 32 * g + 8 * c : 32 * c + 8 * g); };
+  auto at = [&](int k0, int c, bool codes) {
+    if (F8) return k0 + 64 * c + 16 * g;
+    return k0 + (codes ? 32 * g : WM ? 32 * g + 8 * c : 32 * c + 8 * g);
+  };
   auto load = [&](int k0, auto whole_c) {
     constexpr bool whole = decltype(whole_c)::value;
     Turn f;
@@ -97,6 +107,7 @@ __global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(Product
       return in ? v : zero;
     };
     auto scale = [&](const uint8_t* row) {
+      if (F8) return *(const uint32_t*)(row + (int64_t)(k0 / 128) * 4);
       const int b = k0 / 32 + g;
       const bool in = whole || b * 32 < K;
       const uint32_t v = row[in ? b : 0];
@@ -105,19 +116,37 @@ __global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(Product
 #pragma unroll
     for (int b = 0; b < NW; ++b) {
 #pragma unroll
-      for (int c = 0; c < CW; ++c) f.w[b][c] = piece(w[b], at(k0, c, WM), WM ? 2 : 8);
-      if constexpr (WM) f.ws[b] = scale(ws[b]);
+      for (int c = 0; c < CW; ++c) f.w[b][c] = piece(w[b], at(k0, c, WM), F8 ? 4 : WM ? 2 : 8);
+      if constexpr (WM || F8) f.ws[b] = scale(ws[b]);
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
 #pragma unroll
-      for (int c = 0; c < CX; ++c) f.x[i][c] = piece(x[i], at(k0, c, XM), XM ? 2 : 8);
-      if constexpr (XM) f.xs[i] = scale(xs[i]);
+      for (int c = 0; c < CX; ++c) f.x[i][c] = piece(x[i], at(k0, c, XM), F8 ? 4 : XM ? 2 : 8);
+      if constexpr (XM || F8) f.xs[i] = scale(xs[i]);
     }
     return f;
   };
   auto multiply = [&](const Turn& f) {
-    if constexpr (XM) {
+    if constexpr (F8) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        op_bf16x8 xv[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) xv[c] = op_f8x8_values(f.x[i][c >> 1][c % 2 * 2], f.x[i][c >> 1][c % 2 * 2 + 1]);
+#pragma unroll
+        for (int b = 0; b < NW; ++b) {
+          op_f32x4 part = {};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                op_f8x8_values(f.w[b][c >> 1][c % 2 * 2], f.w[b][c >> 1][c % 2 * 2 + 1]), xv[c], part, 0, 0, 0);
+          const float s = __uint_as_float(f.xs[i]) * __uint_as_float(f.ws[b]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i][b][q] = fmaf(s, part[q], acc[i][b][q]);
+        }
+      }
+    } else if constexpr (XM) {
 #pragma unroll
       for (int b = 0; b < NW; ++b) {
         const op_i32x8 wv = {(int)f.w[b][0][0], (int)f.w[b][0][1], (int)f.w[b][0][2], (int)f.w[b][0][3], 0, 0, 0, 0};
@@ -252,7 +281,7 @@ static ProductVariant choose(const ProductArgs& a, bool glu) {
   const int64_t n_out = glu ? a.N / 2 : a.N, rows = a.n_rows / a.n_experts;
   auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * ((n_out + n - 1) / n); };
   // the tile kernels address the rows of x of a tile with 32-bit offsets
-  if (a.x_ld < (1 << 23)) {
+  if (AT != MOE_F8 && a.x_ld < (1 << 23)) {
     const int64_t big = glu ? tiles(256, 128) : tiles(256, 256), half = tiles(128, 128), mid = tiles(64, 128);
     auto rounds = [](int64_t n) { return (n + 255) / 256; };
     const bool use_big = a.n_experts == 1 && !glu
@@ -287,18 +316,21 @@ template <int AT, int WT>
 static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
   const ProductVariant v = choose<AT, WT>(a, glu);
   if (v <= ProductVariant::kSmall64) return glu ? launch_small<AT, WT, true>(a, v, s) : launch_small<AT, WT, false>(a, v, s);
-  if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, v, s);
+  if constexpr (AT == MOE_F8) return hipErrorInvalidValue;
+  else if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, v, s);
   else if constexpr (WT == MOE_MXFP4) return launch_tile_w4(a, glu, v, s);
   else return launch_tile_bf16(a, glu, v, s);
 }
 
 hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool glu, hipStream_t s) {
+  if (x_dtype == MOE_F8) return launch_typed<MOE_F8, MOE_F8>(a, glu, s);
   if (x_dtype == MOE_MXFP4) return launch_typed<MOE_MXFP4, MOE_MXFP4>(a, glu, s);
   return w_dtype == MOE_MXFP4 ? launch_typed<MOE_BF16, MOE_MXFP4>(a, glu, s)
                               : launch_typed<MOE_BF16, MOE_BF16>(a, glu, s);
 }
 
 static ProductVariant product_variant(const ProductArgs& a, int x_dtype, int w_dtype, bool glu) {
+  if (x_dtype == MOE_F8) return choose<MOE_F8, MOE_F8>(a, glu);
   if (x_dtype == MOE_MXFP4) return choose<MOE_MXFP4, MOE_MXFP4>(a, glu);
   return w_dtype == MOE_MXFP4 ? choose<MOE_BF16, MOE_MXFP4>(a, glu) : choose<MOE_BF16, MOE_BF16>(a, glu);
 }
@@ -310,7 +342,7 @@ static ProductVariant product_variant(const ProductArgs& a, int x_dtype, int w_d
 extern "C" int moert_product_variant(int x_dtype, int w_dtype, int glu, int n_experts, int n_rows, int N, int K) {
   if (n_experts < 1 || n_rows < 1 || N < 1 || K < 1) return -1;
   moert::ProductArgs a{};
-  a.x_ld = x_dtype == MOE_MXFP4 ? K / 2 : (int64_t)K * 2;
+  a.x_ld = x_dtype == MOE_F8 ? K : x_dtype == MOE_MXFP4 ? K / 2 : (int64_t)K * 2;
   a.n_experts = n_experts;
   a.n_rows = n_rows;
   a.N = N;

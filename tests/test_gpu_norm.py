@@ -1,0 +1,459 @@
+"""GPU parity of the norms around a block with the fp64 oracle, and the F8 forward
+of a routed block as one chain.
+
+Bounds, in units of u = 2^-24, to first order; every comparison allows 1% more for
+the rest.  A sum of squares: no value passes more than 32 + 4 + 2 + 16 additions and
+one square, all terms positive: 55 u relative; mean, eps, root and reciprocal add 5
+u, of which the sum's part counts half: 33 u on the inverse root.  y = r * inv * weight:
+two roundings more, 35 u.  b: k multiply-adds, (k + 1) u sum|w p|.  An error e
+of a row's values moves its inverse root by at most sum(|v| e) / (sum v^2 + H eps).
+r: gate and scale add 3 u of the summand and 1 u of r.  A BF16 result adds half a step, 2^-8
+of the value, F8 half a step of e4m3: 2^-4 of the value, 2^-10 of the scale where
+codes are subnormal, and the scale's own 3 u."""
+import numpy as np
+import pytest
+
+from oracle import ops as OO
+from tests.harness import log
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def t():
+    import torch
+    return torch
+
+
+@pytest.fixture(scope="module")
+def B():
+    import routed_expert_execution_moe_amd as B
+    return B
+
+
+def _np(x):
+    return x.double().cpu().numpy()
+
+
+def _dev(t, rng, shape, dtype, sigma=1.0, shift=0.0, pad=0):
+    """Random values; pad: columns of NaN behind every row."""
+    a = (rng.standard_normal(shape) * sigma + shift).astype(np.float32)
+    x = t.full((*shape[:-1], shape[-1] + pad), float("nan"), dtype=getattr(t, dtype), device="cuda")
+    x[..., :shape[-1]] = t.from_numpy(a).cuda().to(x.dtype)
+    return x[..., :shape[-1]]
+
+
+def _normed(v, err, weight, eps):
+    """(y, bound) of rows v that are off by err."""
+    y, inv = OO.norm(v, weight, eps)
+    H = v.shape[1]
+    turn = (np.abs(v) * err).sum(1, keepdims=True) / ((v * v).sum(1, keepdims=True) + H * eps)
+    return y, np.abs(inv * weight) * err + np.abs(y) * (turn + 35 * U)
+
+
+def _out(t, T, H, out, pad=0):
+    """(y, y_scales) to write to; pad: columns between the rows, which must stay."""
+    dtype = t.float8_e4m3fn if out == "f8" else getattr(t, out)
+    y = t.full((T, H + pad), 3.0, device="cuda").to(dtype)
+    return y, t.full((T, -(-H // 128)), 9.0, device="cuda") if out == "f8" else None
+
+
+def _close(t, y, ys, want, bound, what):
+    """y (and its scales) against want within bound and the output's rounding."""
+    bound = bound * 1.01 + 1e-37
+    if ys is None:
+        got = _np(y)
+        half = {t.bfloat16: 2.0 ** -8, t.float32: U}[y.dtype]
+        tol = bound + half * (np.abs(want) + bound)
+    else:
+        s = _np(ys)
+        T, H = want.shape
+        wide = np.repeat(s, 128, axis=1)[:, :H]
+        got = _np(y) * wide
+        tol = bound + 2.0 ** -4 * (np.abs(want) + bound) + 2.0 ** -10 * wide + 3 * U * np.abs(got)
+        for b in range(s.shape[1]):
+            part = slice(b * 128, (b + 1) * 128)
+            top = np.abs(want[:, part]).max(1)
+            off = np.abs(s[:, b] * 448 - np.maximum(top, 448 * 2.0 ** -126))
+            assert (off <= bound[:, part].max(1) + 3 * U * top + 1e-37).all(), (what, "scale", b)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], want[bad][:4], tol[bad][:4])
+
+
+WIDTHS = [1, 3, 8, 15, 16, 127, 128, 130, 256, 264, 500, 512, 520, 1000, 2048, 2531, 4096, 7168, 8192, 8200, 12288, 16384, 16400, 32768]
+
+
+@pytest.mark.parametrize("out", ["float32", "bfloat16", "f8"])
+@pytest.mark.parametrize("dtype,weight", [("float32", "bfloat16"), ("bfloat16", "float32"), ("bfloat16", "bfloat16")])
+@pytest.mark.parametrize("H", WIDTHS)
+def test_norm(t, B, H, dtype, weight, out):
+    if out == "f8" and H % 16:
+        return
+    log(f"norm H={H} {dtype} {weight} {out}")
+    rng = np.random.default_rng(H)
+    for T in (1, 2, 37):
+        x, w = _dev(t, rng, (T, H), dtype, 3.0), _dev(t, rng, (H,), weight, 0.1, 1.0)
+        y, ys = _out(t, T, H, out)
+        B.moe_norm(x, w, y, y_scales=ys, eps=1e-5)
+        want, bound = _normed(_np(x), 0.0, _np(w), float(np.float32(1e-5)))
+        _close(t, y, ys, want, bound, (H, T))
+
+
+@pytest.mark.parametrize("H", [16, 144, 512, 1040, 8208, 16400])
+def test_f8_rows_are_the_fp32_rows_converted(t, B, H):
+    """Bit for bit what moe_f8_quantize makes of the fp32 output."""
+    log(f"norm f8 {H}")
+    rng = np.random.default_rng(H)
+    x, w = _dev(t, rng, (70, H), "bfloat16", 5.0), _dev(t, rng, (H,), "bfloat16", 0.1, 1.0)
+    x[3] = 0
+    x[4, H // 2] = float("inf")
+    x[5, 1] = float("nan")
+    x[6] *= 1e-30
+    f, c, q = (t.empty((70, H), dtype=d, device="cuda") for d in (t.float32, t.float8_e4m3fn, t.float8_e4m3fn))
+    s, qs = (t.empty((70, -(-H // 128)), device="cuda") for _ in range(2))
+    B.moe_norm(x, w, f)
+    B.moe_norm(x, w, c, y_scales=s)
+    B.moe_f8_quantize(f, q, qs)
+    assert t.equal(c.view(t.uint8), q.view(t.uint8)) and t.equal(s.nan_to_num(-1), qs.nan_to_num(-1))
+    assert bool(s[5].isnan().all()) and bool((f[3] == 0).all())
+
+
+@pytest.mark.parametrize("H", [40, 144, 520, 2080, 9008])
+def test_norm_strided_and_unaligned(t, B, H):
+    """Rows at any element's alignment with NaN between them; what lies between the rows of y stays."""
+    log(f"norm strided {H}")
+    rng = np.random.default_rng(H)
+    T = 21
+    for dtype in ("float32", "bfloat16"):
+        for out in ("float32", "bfloat16", "f8"):
+            if out == "f8" and H % 16:
+                continue
+            x = _dev(t, rng, (T, H + 1), dtype, 1.0, pad=2)[:, 1:]
+            w = _dev(t, rng, (H + 1,), dtype, 0.1, 1.0)[1:]
+            pad = 16 if out == "f8" else 3
+            y, ys = _out(t, T, H, out, pad)
+            lo = 0 if out == "f8" else 1
+            B.moe_norm(x, w, y[:, lo:lo + H], y_scales=ys)
+            want, bound = _normed(_np(x), 0.0, _np(w), float(np.float32(1e-6)))
+            _close(t, y[:, lo:lo + H], ys, want, bound, (H, dtype, out))
+            rest = t.cat([y[:, :lo], y[:, lo + H:]], 1)
+            assert bool((rest.float() == 3).all())
+
+
+def test_norm_ends_of_the_range(t, B):
+    """Rows of zeros, of the smallest and of large values; some whose squares leave fp32; infinities and NaN stay in their rows."""
+    log("norm ends")
+    for H in (64, 300, 2048):
+        x = t.ones((8, H), device="cuda")
+        x[0] = 0
+        x[1] = 2.0 ** -140
+        x[2] = 1e18
+        x[3] = 1e20
+        x[4, 5] = float("inf")
+        x[5, 7] = float("nan")
+        x[6] = -2.0
+        w = t.full((H,), 0.5, device="cuda")
+        y = t.full((8, H), 9.0, device="cuda")
+        B.moe_norm(x, w, y)
+        got = y.cpu()
+        assert bool((got[0] == 0).all()) and bool((got[1].abs() < 1e-36).all())
+        assert bool(((got[2:4] - 0.5).abs() < 1e-6).all())
+        assert bool(got[4, 5].isnan()) and bool((got[4, :5] == 0).all()) and bool(got[5].isnan().all())
+        assert bool(((got[6] + 0.5).abs() < 1e-6).all()) and bool(((got[7] - 0.5).abs() < 1e-6).all())
+
+
+@pytest.mark.parametrize("H", [8, 600])
+def test_norm_more_rows_than_workgroups(t, B, H):
+    log(f"norm many rows {H}")
+    T = (1 << 24) + 37 if H == 8 else (1 << 20) + 5
+    x = t.arange(T, device="cuda").remainder(7).add(1).to(t.bfloat16)[:, None].expand(T, H).contiguous()
+    y = t.empty_like(x)
+    B.moe_norm(x, t.ones(H, device="cuda"), y)
+    assert float((y.float() - 1).abs().max()) < 2 ** -8
+
+
+@pytest.mark.parametrize("H", [16, 520, 2048, 20000])
+def test_rows_whose_squares_leave_fp32(t, B, H):
+    """Up to the largest values, in front of the sums, after them, and in F8."""
+    log(f"norm large {H}")
+    rng = np.random.default_rng(H)
+    x = _dev(t, rng, (6, H), "float32").clamp(-3, 3) * t.tensor([1e18, 1e22, 1e30, 1e37, 1.1e38, 1.0], device="cuda")[:, None]
+    x[4, H // 2] = 3.4e38
+    w = _dev(t, rng, (H,), "float32", 0.1, 1.0)
+    want, bound = _normed(_np(x), 0.0, _np(w), float(np.float32(1e-6)))
+    for out in ("float32", "f8"):
+        if out == "f8" and H % 16:
+            continue
+        y, ys = _out(t, 6, H, out)
+        B.moe_norm(x, w, y, y_scales=ys)
+        _close(t, y, ys, want, bound, (H, out))
+    c = dict(p=x, w=None, residual=_dev(t, rng, (6, H), "float32"), scale=0.5, weight=w, post_weight=w)
+    _check(t, B, c, "float32", ("post", H))
+
+
+# ------------------------------------------------------------------ the end of a block
+def _case(t, rng, T, k, H, p="float32", res="bfloat16", weight="bfloat16", gate=None, gate_dtype="float32", post=True, E=0, pad=0):
+    c = dict(p=_dev(t, rng, (T * k, H), p, 0.7, pad=pad), residual=_dev(t, rng, (T, H), res, 2.0, pad=pad),
+             w=t.softmax(_dev(t, rng, (T, k), "float32"), 1), scale=0.3,
+             weight=_dev(t, rng, (H,), weight, 0.1, 1.0), post_weight=_dev(t, rng, (H,), weight, 0.1, 1.0) if post else None)
+    if gate:
+        c["gate"] = t.sigmoid(_dev(t, rng, (T if gate in ("token", "both") else 1, H if gate in ("channel", "both") else 1), gate_dtype))
+    if E:
+        c["ids"] = t.from_numpy(rng.integers(-2, E + 2, (T, k)).astype(np.int32)).cuda()
+        c["ids"][T // 2] = -1  # a token without any
+        c["n_experts"] = E
+        bad = (c["ids"] < 0) | (c["ids"] >= E)
+        c["p"].view(T, k, H)[bad] = float("nan") if not pad else 0  # rows that must not be read
+    return c
+
+
+def _want(c, eps):
+    """((r, bound), (y, bound)) of the formulas in fp64."""
+    T, H = c["residual"].shape
+    k = 1 if c["w"] is None else c["w"].shape[1]
+    w = np.ones((T, k)) if c["w"] is None else _np(c["w"])
+    ids = None if "ids" not in c else c["ids"].cpu().numpy()
+    b, mag = OO.combine(np.nan_to_num(_np(c["p"])) if ids is not None else _np(c["p"]), w, ids, c.get("n_experts", 0))
+    err = (k + 1) * U * mag
+    if c["post_weight"] is not None:
+        b, err = _normed(b, err, _np(c["post_weight"]), eps)
+    g = float(np.float32(c["scale"])) * (_np(c["gate"]) if c.get("gate") is not None else 1.0)
+    r = _np(c["residual"]) + g * b
+    err = np.abs(g) * (err + 3 * U * np.abs(b)) + U * np.abs(r)
+    return (r, err), _normed(r, err, _np(c["weight"]), eps)
+
+
+def _check(t, B, c, out, what, eps=1e-6, pad=0):
+    T, H = c["residual"].shape
+    y, ys = _out(t, T, H, out, pad)
+    after = t.full((T, H + pad), 3.0, dtype=c["residual"].dtype, device="cuda")
+    B.moe_combine_norm(out=after[:, :H], y=y[:, :H], y_scales=ys, eps=eps, **c)
+    r, n = _want(c, float(np.float32(eps)))
+    _close(t, after[:, :H], None, *r, (*what, "out"))
+    _close(t, y[:, :H], ys, *n, (*what, "y"))
+    if pad:
+        assert bool((after[:, H:] == 3).all()) and bool((y[:, H:].float() == 3).all())
+    return after, y, ys
+
+
+@pytest.mark.parametrize("k", [1, 3, 8, 17])
+@pytest.mark.parametrize("H", [1, 16, 130, 272, 520, 2048, 2531, 8192, 8208, 20000, 32768])
+def test_combine_norm(t, B, H, k):
+    rng = np.random.default_rng(H * 31 + k)
+    n = 0
+    for p in ("float32", "bfloat16"):
+        for gate in (None, "token", "channel", "both"):
+            for post in (False, True):
+                n += 1
+                out = ("float32", "bfloat16", "f8")[n % 3 if H % 16 == 0 else n % 2]
+                log(f"combine_norm H={H} k={k} {p} gate={gate} post={post} {out}")
+                T = (1, 9, 30)[n % 3]
+                c = _case(t, rng, T, k, H, p, ("bfloat16", "float32")[n // 2 % 2], ("float32", "bfloat16")[n // 4 % 2], gate,
+                          ("float32", "bfloat16")[n % 2], post, E=5 if n % 2 else 0)
+                _check(t, B, c, out, (H, k, p, gate, post))
+
+
+@pytest.mark.parametrize("H", [40, 144, 1040, 9008])
+def test_combine_norm_strided(t, B, H):
+    log(f"combine_norm strided {H}")
+    rng = np.random.default_rng(H)
+    for out in ("float32", "bfloat16", "f8"):
+        if out == "f8" and H % 16:
+            continue
+        c = _case(t, rng, 11, 4, H, "bfloat16", gate="both", pad=16)
+        big = t.full((22, H + 5), float("nan"), device="cuda")
+        big[::2, 2:H + 2] = c["gate"]
+        c["gate"] = big[::2, 2:H + 2]
+        _check(t, B, c, out, (H, out), pad=16)
+
+
+def test_combine_norm_of_a_plain_block(t, B):
+    """w None: the block's own rows; no weight: the residual alone; what the parts alone give, bit for bit."""
+    log("combine_norm plain")
+    rng = np.random.default_rng(3)
+    for T, H in ((5, 2048), (300, 520), (64, 96)):
+        c = _case(t, rng, T, 1, H, "bfloat16", post=False)
+        c["w"] = None
+        after, y, _ = _check(t, B, c, "float32", (T, H))
+        alone = t.empty_like(after)
+        B.moe_combine_norm(c["p"], None, c["residual"], alone, scale=c["scale"])
+        assert t.equal(alone, after)
+        r = t.empty((T, H), device="cuda")
+        B.moe_combine_norm(c["p"], None, c["residual"], r, scale=c["scale"])
+        again = t.empty_like(y)
+        B.moe_norm(r, c["weight"], again)
+        assert t.equal(again, y)  # y comes from the fp32 residual, not from its rounding
+
+
+def test_combine_norm_in_place(t, B):
+    log("combine_norm in place")
+    rng = np.random.default_rng(4)
+    for T, k, H in ((3, 8, 2048), (200, 2, 136), (40, 4, 9008)):
+        c = _case(t, rng, T, k, H, E=6, gate="channel")
+        after, y, ys = _check(t, B, c, "bfloat16", (T, k, H))
+        y2 = t.empty_like(y)
+        residual = c.pop("residual").clone()
+        B.moe_combine_norm(residual=residual, out=residual, y=y2, **c)
+        assert t.equal(residual, after) and t.equal(y2, y)
+
+
+def test_combine_norm_without_experts(t, B):
+    """Tokens that no expert serves keep their residual, whatever lies in their rows and weights."""
+    log("combine_norm no experts")
+    rng = np.random.default_rng(5)
+    for post in (False, True):
+        for H in (96, 2048):
+            c = _case(t, rng, 6, 4, H, gate="token", post=post)
+            c["p"].fill_(float("nan"))
+            c["w"].fill_(float("inf"))
+            c["ids"] = t.full((6, 4), -1, dtype=t.int32, device="cuda")
+            after, y = t.empty_like(c["residual"]), t.empty((6, H), device="cuda")
+            B.moe_combine_norm(out=after, y=y, n_experts=9, **c)
+            assert t.equal(after, c["residual"])
+            want, bound = _normed(_np(c["residual"]), 0.0, _np(c["weight"]), float(np.float32(1e-6)))
+            _close(t, y, None, want, bound, (post, H))
+
+
+def test_combine_norm_agrees_with_combine_pairs(t, B):
+    """Without norm, gate and residual the sum is moe_combine_pairs', bit for bit."""
+    log("combine_norm sum")
+    rng = np.random.default_rng(6)
+    for T, k, H, p in ((9, 8, 2048, "float32"), (50, 5, 333, "bfloat16"), (4, 20, 17000, "float32")):
+        c = _case(t, rng, T, k, H, p, E=7)
+        a, b = t.empty((T, H), device="cuda"), t.empty((T, H), device="cuda")
+        B.moe_combine_pairs(c["p"], c["w"], a, ids=c["ids"], n_experts=7)
+        B.moe_combine_norm(c["p"], c["w"], t.zeros((T, H), device="cuda"), b, ids=c["ids"], n_experts=7)
+        assert t.equal(a, b)
+
+
+def test_no_rows(t, B):
+    log("no rows")
+    e = lambda *s, **k: t.empty(s, device="cuda", **k)  # noqa: E731
+    B.moe_norm(e(0, 64), e(64), e(0, 64))
+    B.moe_combine_norm(e(0, 64), e(0, 3), e(0, 64), e(0, 64), weight=e(64), y=e(0, 64), post_weight=e(64), gate=e(1, 64))
+    B.moe_f8_quantize(e(0, 64), e(0, 64, dtype=t.float8_e4m3fn), e(0, 1))
+    B.moe_f8_gemm(e(0, 64, dtype=t.float8_e4m3fn), e(0, 1), e(5, 64).to(t.float8_e4m3fn), e(1, 1), e(0, 5))
+    t.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ a routed block
+class Block:
+    """norm -> route -> group -> gate/up -> convert -> down -> sum, residual and the next norm, on caller-held buffers."""
+
+    def __init__(self, t, B, rng, T, k, E, H, I):
+        f8 = t.float8_e4m3fn
+        self.t, self.B, self.k, self.E = t, B, k, E
+        e = lambda *s, dtype=t.float32: t.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+        self.x = _dev(t, rng, (T, H), "bfloat16", 2.0)
+        self.norms = [_dev(t, rng, (H,), "bfloat16", 0.1, 1.0) for _ in range(3)]
+        up, down = _dev(t, rng, (E * 2, I, H), "float32", 0.05), _dev(t, rng, (E, H, I), "float32", 0.05)
+        self.up, self.ups = e(E * 2, I, H, dtype=f8), e(E * 2, -(-I // 128), -(-H // 128))
+        self.down, self.downs = e(E, H, I, dtype=f8), e(E, -(-H // 128), -(-I // 128))
+        B.moe_f8_quantize(up, self.up, self.ups, block_rows=128)
+        B.moe_f8_quantize(down, self.down, self.downs, block_rows=128)
+        self.up, self.ups = self.up.view(E, 2 * I, H), self.ups.view(E, -1, self.ups.shape[2])
+        ids = np.argsort(-rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+        ids[-1] = -1  # a padded token
+        self.ids = t.from_numpy(ids).cuda()
+        self.w = t.softmax(_dev(t, rng, (T, k), "float32"), 1)
+        self.h, self.hs = e(T, H, dtype=f8), e(T, -(-H // 128))
+        self.offsets, self.perm = e(E + 1, dtype=t.int32), e(T * k, dtype=t.int32)
+        self.ws = e(max(1, B.moe_group_workspace(T, k, E)), dtype=t.uint8)
+        self.mid = e(T * k, I, dtype=t.bfloat16)
+        self.q, self.qs = e(T * k, I, dtype=f8), e(T * k, -(-I // 128))
+        self.p = e(T * k, H, dtype=t.bfloat16)
+        self.out, self.y = e(T, H, dtype=t.bfloat16), e(T, H, dtype=t.bfloat16)
+        self.mid.zero_()
+
+    def __call__(self, stream=None):
+        B = self.B
+        B.moe_norm(self.x, self.norms[0], self.h, y_scales=self.hs, stream=stream)
+        B.moe_group_pairs(self.ids, self.E, self.offsets, self.perm, workspace=self.ws, stream=stream)
+        B.moe_grouped_gemm(self.h, self.up, self.offsets, self.mid, x_scales=self.hs, w_scales=self.ups, x_index=self.perm,
+                           x_index_div=self.k, glu=True, stream=stream)
+        B.moe_f8_quantize(self.mid, self.q, self.qs, stream=stream)
+        B.moe_grouped_gemm(self.q, self.down, self.offsets, self.p, x_scales=self.qs, w_scales=self.downs, y_index=self.perm,
+                           stream=stream)
+        B.moe_combine_norm(self.p, self.w, self.x, self.out, ids=self.ids, n_experts=self.E, post_weight=self.norms[1], scale=0.5,
+                           weight=self.norms[2], y=self.y, stream=stream)
+        return self.out, self.y
+
+    def want(self):
+        """The block from its formulas in fp64, on the values that the codes of each step stand for."""
+        T, H = self.x.shape
+        h = OO.f8_values(self.h.view(self.t.uint8).cpu().numpy(), self.hs.cpu().numpy())
+        b = np.zeros((T, H))
+        ids, w = self.ids.cpu().numpy(), _np(self.w)
+        up, ups, down, downs = (a.cpu().numpy() for a in (self.up.view(self.t.uint8), self.ups, self.down.view(self.t.uint8), self.downs))
+        for e in range(self.E):
+            hit = np.argwhere(ids == e)
+            if not len(hit):
+                continue
+            I, n = up.shape[1] // 2, ups.shape[1] // 2
+            g, u = (OO.f8_values(up[e, s], ups[e, c], 128) for s, c in ((slice(0, I), slice(0, n)), (slice(I, None), slice(n, None))))
+            a = h[hit[:, 0]]
+            m = OO.silu(a @ g.T) * (a @ u.T)
+            np.add.at(b, hit[:, 0], w[hit[:, 0], hit[:, 1], None] * (m @ OO.f8_values(down[e], downs[e], 128).T))
+        n = OO.norm(b, _np(self.norms[1]), 1e-6)[0]
+        r = _np(self.x) + 0.5 * n
+        return r, OO.norm(r, _np(self.norms[2]), 1e-6)[0]
+
+
+BLOCKS = [(1, 4, 8, 272, 144), (9, 8, 32, 2048, 768), (400, 4, 8, 1040, 528), (1500, 8, 16, 768, 256)]
+
+
+@pytest.mark.parametrize("T,k,E,H,I", BLOCKS)
+def test_routed_block(t, B, T, k, E, H, I):
+    """The chain against fp64.  Between the products the rows are rounded to e4m3 (2^-4 of a value at most, about
+    2^-5.4 in the root mean square, independently), so the block's part is off by that share of its size."""
+    log(f"block {T}x{k} E{E} {H} {I}")
+    b = Block(t, B, np.random.default_rng(T), T, k, E, H, I)
+    out, y = b()
+    r, want = b.want()
+    served = np.arange(T) < T - 1 if T > 1 else np.zeros(1, bool)
+    assert t.equal(out[~t.from_numpy(served).cuda()], b.x[~t.from_numpy(served).cuda()])
+    part = np.sqrt(((r - _np(b.x)) ** 2).mean())
+    off = np.sqrt(((_np(out) - r) ** 2).mean())
+    assert off <= 2.0 ** -4 * part + 2.0 ** -8 * np.sqrt((r ** 2).mean())
+    assert np.sqrt(((_np(y) - want) ** 2).mean()) <= 2.0 ** -3 * np.sqrt((want ** 2).mean()) * (part / np.sqrt((r ** 2).mean()) + 2.0 ** -5)
+
+
+def test_routed_blocks_on_streams_and_in_graphs(t, B):
+    """Several blocks at once on streams of their own, and captured and replayed with eager work between the
+    replays: bit for bit the eager result, on new inputs too."""
+    log("blocks on streams")
+    blocks = [Block(t, B, np.random.default_rng(50 + i), *BLOCKS[i]) for i in (1, 2, 3)]
+    want = [[v.clone() for v in b()] for b in blocks]
+    t.cuda.synchronize()
+    streams = [t.cuda.Stream() for _ in blocks]
+    for _ in range(3):
+        for b, s in zip(blocks, streams):
+            b.out.zero_(), b.y.zero_()
+        t.cuda.synchronize()
+        for b, s in zip(blocks, streams):
+            b(stream=s)
+        t.cuda.synchronize()
+        for b, w in zip(blocks, want):
+            assert t.equal(b.out, w[0]) and t.equal(b.y, w[1])
+    graphs = []
+    for b in blocks:
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            b()
+        graphs.append(g)
+    kept = [b.x.clone() for b in blocks]
+    for i in range(4):
+        for b, g, x in zip(blocks, graphs, kept):
+            b.x.copy_(x if i % 2 else x.flip(0))
+            b.out.zero_(), b.y.zero_()
+        for g in graphs:
+            g.replay()
+        t.cuda.synchronize()
+        got = [(b.out.clone(), b.y.clone()) for b in blocks]
+        for b, (o, y) in zip(blocks, got):
+            b.out.zero_()
+            eager = b()
+            assert t.equal(eager[0], o) and t.equal(eager[1], y)
+        if i % 2:
+            assert all(t.equal(o, w[0]) for (o, _), w in zip(got, want))
