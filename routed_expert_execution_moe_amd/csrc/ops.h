@@ -83,6 +83,8 @@ enum class ProductVariant { kSmall16, kSmall32, kSmall64, kDeep, kShared, kHalf,
 hipError_t launch_tile_bf16(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s);
 hipError_t launch_tile_w4(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s);
 hipError_t launch_tile_mx(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s);
+// F8 (product_f8.hip): Shared (64 x 128), Half (128 x 128), and with BF16 y Big (256 x 256)
+hipError_t launch_tile_f8(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s);
 size_t group_workspace(int64_t pairs, int E);
 hipError_t launch_group_pairs(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* perm,
                               int32_t* ws, hipStream_t s);

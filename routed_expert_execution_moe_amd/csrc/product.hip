@@ -231,6 +231,25 @@ static hipError_t launch_small_as(const ProductArgs& a, hipStream_t s) {
   return launch_op(product_small_kernel<AT, WT, GLU, MI, NB>, dim3((unsigned)wgs), dim3(kSmWaves * 64), s, a);
 }
 
+// Which variant of an F8 product, by the tiles that a call can make at most and by
+// the mean rows of an expert.
+static ProductVariant choose_f8(const ProductArgs& a, bool glu) {
+  const int64_t n_out = glu ? a.N / 2 : a.N, rows = a.n_rows / a.n_experts;
+  auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * ((n_out + n - 1) / n); };
+  // the tile kernels address the rows of x of a tile with 32-bit offsets
+  if (a.x_ld < (1 << 23)) {
+    const int g = glu ? 2 : 1;
+    if (!a.y_f32 && tiles(256, 256 / g) >= 128 && rows >= 128) return ProductVariant::kBig;
+    if (tiles(128, 128 / g) > 256 && rows >= 64) return ProductVariant::kHalf;
+    if (tiles(64, 128 / g) >= 64 && a.n_rows > 8) return ProductVariant::kShared;
+  }
+  const int groups = std::min(a.n_experts, a.n_rows);
+  const int avg = (a.n_rows + groups - 1) / groups;
+  if (avg <= 16 || tiles(16, 16) <= 512) return ProductVariant::kSmall16;
+  if (avg <= 64 || tiles(32, 16) <= 512) return ProductVariant::kSmall32;
+  return ProductVariant::kSmall64;
+}
+
 // Which variant, by the tiles that a call can make at most and by the mean rows
 // of an expert (us on MI355X; "up" is a GLU product of N = 1536, K = 2048 over 128
 // experts, "plain" one without GLU of N = 2048, K = 768, both with 8 experts a
@@ -277,11 +296,12 @@ static hipError_t launch_small_as(const ProductArgs& a, hipStream_t s) {
 //       rows 128, 121 | 130, 191; 429, 414 | 428, 416; 825, 761 | 826, 753.
 template <int AT, int WT>
 static ProductVariant choose(const ProductArgs& a, bool glu) {
+  if constexpr (AT == MOE_F8) return choose_f8(a, glu);
   constexpr bool XM = AT == MOE_MXFP4, W4 = !XM && WT == MOE_MXFP4;
   const int64_t n_out = glu ? a.N / 2 : a.N, rows = a.n_rows / a.n_experts;
   auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * ((n_out + n - 1) / n); };
   // the tile kernels address the rows of x of a tile with 32-bit offsets
-  if (AT != MOE_F8 && a.x_ld < (1 << 23)) {
+  if (a.x_ld < (1 << 23)) {
     const int64_t big = glu ? tiles(256, 128) : tiles(256, 256), half = tiles(128, 128), mid = tiles(64, 128);
     auto rounds = [](int64_t n) { return (n + 255) / 256; };
     const bool use_big = a.n_experts == 1 && !glu
@@ -316,7 +336,7 @@ template <int AT, int WT>
 static hipError_t launch_typed(const ProductArgs& a, bool glu, hipStream_t s) {
   const ProductVariant v = choose<AT, WT>(a, glu);
   if (v <= ProductVariant::kSmall64) return glu ? launch_small<AT, WT, true>(a, v, s) : launch_small<AT, WT, false>(a, v, s);
-  if constexpr (AT == MOE_F8) return hipErrorInvalidValue;
+  if constexpr (AT == MOE_F8) return launch_tile_f8(a, glu, v, s);
   else if constexpr (AT == MOE_MXFP4) return launch_tile_mx(a, glu, v, s);
   else if constexpr (WT == MOE_MXFP4) return launch_tile_w4(a, glu, v, s);
   else return launch_tile_bf16(a, glu, v, s);
