@@ -8,6 +8,10 @@
 // always in the same order.  Rows of up to 512 columns share a workgroup, 16, 32 or
 // 64 threads each; a longer one has its own.  F8 rows are converted from the same
 // registers: 16 neighbouring lanes hold a block of 128 columns.
+//
+// HBM bounds both: 8192 tokens of 8 fp32 rows of 4,096, normed, gated, added and normed again,
+// 238 us, 5.3 TB/s (a plain copy reaches 5.2); norm of 8192 x 4096 bf16 to F8 25.0 us,
+// 4.1 TB/s, whose rows are too short a work for a workgroup to hide its own start.
 #include "ops.h"
 
 namespace moert {
@@ -40,19 +44,30 @@ __device__ inline float norm_sum(float v, int lg, float* red) {
   return v;
 }
 
-template <bool CLOSE, bool PF32, int NV>
+// UNI: a wave's lanes belong to one row, whose index is a scalar then.  WIDE: H is 8
+// at least.  A piece that would pass the row's end is the row's last 8 columns
+// then, of which the first lo are other lanes': so every load is one access, and
+// lanes without a column of their own go along.
+template <bool CLOSE, bool PF32, int NV, bool UNI, bool WIDE>
 __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
   constexpr int PB = PF32 ? 4 : 2;
+  constexpr bool Early = NV == 1;  // weights and gate are requested with the row: one latency
   __shared__ float s_red[2][kNormMost / 64];
-  const bool own = a.lg >= 7;  // the workgroup's one row
+  const bool own = UNI && a.lg >= 7;  // the workgroup's one row
   const int G = own ? (int)blockDim.x : 1 << a.lg;
   const int t = own ? threadIdx.x : threadIdx.x & (G - 1);
-  const int sub = own ? 0 : threadIdx.x >> a.lg, per = own ? 1 : blockDim.x >> a.lg;
+  const int sub = own ? 0 : UNI ? __builtin_amdgcn_readfirstlane(threadIdx.x >> a.lg) : threadIdx.x >> a.lg;
+  const int per = own ? 1 : blockDim.x >> a.lg;
   const int H = a.H;
-  int n[NV];  // columns of each piece, 0 and fewer past the row's end
+  int col[NV], lo[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) n[i] = H - (i * G + t) * 8;
-  auto col = [&](int i) { return (int64_t)(i * G + t) * 8; };
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * G + t) * 8;
+    col[i] = WIDE ? min(c, H - 8) : c;
+    lo[i] = min(c - col[i], 8);
+  }
+  // columns of piece i that are this thread's
+  auto mine = [&](int i, int c) { return WIDE ? c >= lo[i] : col[i] + c < H; };
 
   int slot = 0;
   auto mean_square = [&](const float (&v)[NV][8]) {
@@ -61,7 +76,7 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        if (c < n[i]) sum = fmaf(v[i][c], v[i][c], sum);
+        if (mine(i, c)) sum = fmaf(v[i][c], v[i][c], sum);
     slot ^= 1;
     return norm_sum(sum, a.lg, s_red[slot]) / (float)H;
   };
@@ -79,41 +94,61 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
     }
     return 1.f / sqrtf(ms);
   };
+  auto load = [&](const uint8_t* row, bool f32, int i) {
+    return WIDE ? op_cols_load(row, f32, col[i]) : op_cols_load(row, f32, col[i], H - col[i]);
+  };
+  auto store = [&](uint8_t* row, bool f32, int i, const float (&v)[8]) {
+    if (WIDE) op_cols_store_from(row, f32, col[i], lo[i], v);
+    else op_cols_store(row, f32, col[i], H - col[i], v);
+  };
 
   for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.T; row0 += (int64_t)gridDim.x * per) {
     const int64_t row = row0 + sub;
     const bool live = row < a.T;  // lanes without a row go along, for the barriers
+    const int64_t at = live ? row : 0;
     float r[NV][8];
+    OpCols weight[NV];
+    if (Early && a.weight)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) weight[i] = load(a.weight, a.weight_f32, i);
     if constexpr (!CLOSE) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        op_cols_get(op_cols_load(a.p + (live ? row : 0) * a.ldp * PB, PF32, col(i), live ? n[i] : 0), PF32, r[i]);
+      for (int i = 0; i < NV; ++i) op_cols_get(load(a.p + at * a.ldp * PB, PF32, i), PF32, r[i]);
     } else {
-      OpCols res[NV];
+      const uint8_t* const gate = a.gate ? a.gate + at * a.ldg * (a.gate_f32 ? 4 : 2) : nullptr;
+      OpCols res[NV], post[NV], gates[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        res[i] = op_cols_load(a.res + (live ? row : 0) * a.ldres * (a.res_f32 ? 4 : 2), a.res_f32, col(i), live ? n[i] : 0);
+      for (int i = 0; i < NV; ++i) {
+        res[i] = load(a.res + at * a.ldres * (a.res_f32 ? 4 : 2), a.res_f32, i);
+        if (Early && a.post) post[i] = load(a.post, a.post_f32, i);
+        if (Early && a.gate_cols > 1) gates[i] = load(gate, a.gate_f32, i);
+      }
+      float g0 = 1.f;
+      if (a.gate_cols == 1) g0 = a.gate_f32 ? *(const float*)gate : __uint_as_float((uint32_t)*(const uint16_t*)gate << 16);
       float b[NV][8] = {};
-      constexpr int J = NV == 1 ? 8 : NV == 2 ? 4 : 2;  // expert rows requested before the first is added
+      // Expert rows requested before the first is added.  Eight columns of four fp32 rows
+      // are 32 registers, of eight 64, which with the rest pass the 128 that 1,024
+      // threads leave: 8192 x 8 x 4096 238 us, 316 with eight rows.
+      constexpr int J = !WIDE ? 1 : 4 / NV;
       for (int j0 = 0; live && j0 < a.k; j0 += J) {
         OpCols v[J][NV];
         float w[J];
         bool ok[J];
 #pragma unroll
         for (int q = 0; q < J; ++q) {
-          const int64_t p = row * a.k + j0 + q;
+          const int64_t p = row * a.k + min(j0 + q, a.k - 1);
           ok[q] = j0 + q < a.k;
-          if (ok[q] && a.ids) {
+          if (a.ids) {
             const int e = a.ids[p];
-            ok[q] = e >= 0 && e < a.E;
+            ok[q] = ok[q] && e >= 0 && e < a.E;
           }
-          w[q] = 1.f;
-          if (ok[q]) {
-            if (a.w) w[q] = a.w[p];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) v[q][i] = op_cols_load(a.p + p * a.ldp * PB, PF32, col(i), n[i]);
-          }
+          w[q] = a.w ? a.w[p] : 1.f;
         }
+#pragma unroll
+        for (int q = 0; q < J; ++q)
+          if (ok[q])
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[q][i] = load(a.p + (row * a.k + j0 + q) * a.ldp * PB, PF32, i);
 #pragma unroll
         for (int q = 0; q < J; ++q)
           if (ok[q])
@@ -130,19 +165,16 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           float f[8];
-          op_cols_get(op_cols_load(a.post, a.post_f32, col(i), n[i]), a.post_f32, f);
+          op_cols_get(Early ? post[i] : load(a.post, a.post_f32, i), a.post_f32, f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) b[i][c] = b[i][c] * inv * f[c];
         }
       }
-      const uint8_t* const gate = a.gate ? a.gate + (live ? row : 0) * a.ldg * (a.gate_f32 ? 4 : 2) : nullptr;
-      float g0 = 1.f;
-      if (a.gate_cols == 1) g0 = a.gate_f32 ? *(const float*)gate : __uint_as_float((uint32_t)*(const uint16_t*)gate << 16);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (a.gate_cols > 1) {
           float f[8];
-          op_cols_get(op_cols_load(gate, a.gate_f32, col(i), n[i]), a.gate_f32, f);
+          op_cols_get(Early ? gates[i] : load(gate, a.gate_f32, i), a.gate_f32, f);
 #pragma unroll
           for (int c = 0; c < 8; ++c) b[i][c] *= f[c];
         } else {
@@ -153,7 +185,7 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
         op_cols_get(res[i], a.res_f32, f);
 #pragma unroll
         for (int c = 0; c < 8; ++c) r[i][c] = fmaf(a.scale, b[i][c], f[c]);
-        if (live) op_cols_store(a.out + row * a.ldout * (a.out_f32 ? 4 : 2), a.out_f32, col(i), n[i], r[i]);
+        if (live) store(a.out + row * a.ldout * (a.out_f32 ? 4 : 2), a.out_f32, i, r[i]);
       }
       if (!a.weight) continue;
     }
@@ -162,7 +194,7 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[8];
-      op_cols_get(op_cols_load(a.weight, a.weight_f32, col(i), n[i]), a.weight_f32, f);
+      op_cols_get(Early ? weight[i] : load(a.weight, a.weight_f32, i), a.weight_f32, f);
       uint32_t top = 0;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -170,13 +202,14 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
         top = max(top, __float_as_uint(r[i][c]) & 0x7FFFFFFFu);
       }
       if (a.y_dtype != MOE_F8) {
-        if (live) op_cols_store(a.y + row * a.ldy * (a.y_dtype == MOE_F32 ? 4 : 2), a.y_dtype == MOE_F32, col(i), n[i], r[i]);
+        if (live) store(a.y + row * a.ldy * (a.y_dtype == MOE_F32 ? 4 : 2), a.y_dtype == MOE_F32, i, r[i]);
       } else {
-        const OpF8Scale s(op_max16(n[i] > 0 ? top : 0));
+        // H is a multiple of 16: pieces are whole or nobody's
+        const OpF8Scale s(op_max16(lo[i] == 0 ? top : 0));
         const uint2 q = op_f8x8(r[i], s);
-        if (live && n[i] > 0) {
-          *(uint2*)(a.y + row * a.ldy + col(i)) = q;
-          if ((threadIdx.x & 15) == 0) a.ys[row * ((H + 127) >> 7) + (col(i) >> 7)] = s.scale;
+        if (live && lo[i] == 0) {
+          *(uint2*)(a.y + row * a.ldy + col[i]) = q;
+          if ((threadIdx.x & 15) == 0) a.ys[row * ((H + 127) >> 7) + (col[i] >> 7)] = s.scale;
         }
       }
     }
@@ -185,18 +218,27 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
 
 template <bool CLOSE, bool PF32>
 static hipError_t norm_typed(NormArgs& a, hipStream_t s) {
+  // Two pieces a thread from 1,024 columns on, four past 8,192: fewer waves wait at a
+  // row's barriers.  One and two pieces: norm 8192 x 4096 bf16 to F8 31.5 and 25.0 us, end of
+  // a block 8192 x 2 x 2048 bf16 54 and 44 (four: norm 27.0); two and four: norm 4096
+  // x 16384 64.6 and 56.5.  fp32 rows, which bring twice the bytes a column, one
+  // piece up to 4,096 columns: 8192 x 8 x 4096 238 and 248.
   const int pieces = (a.H + 7) / 8;
   int threads = kNormShared, nv = 1;
   if (pieces <= 64) {
     a.lg = pieces <= 16 ? 4 : pieces <= 32 ? 5 : 6;
   } else {
-    nv = pieces <= kNormMost ? 1 : pieces <= 2 * kNormMost ? 2 : 4;
+    nv = pieces <= (CLOSE && PF32 ? 512 : 128) ? 1 : pieces <= 1024 ? 2 : 4;
     threads = (pieces + nv * 64 - 1) / (nv * 64) * 64;
     a.lg = 10;
   }
   const int64_t per = a.lg < 7 ? threads >> a.lg : 1;
   const dim3 grid((unsigned)std::min<int64_t>((a.T + per - 1) / per, 1 << 20));
-  auto k = nv == 1 ? norm_kernel<CLOSE, PF32, 1> : nv == 2 ? norm_kernel<CLOSE, PF32, 2> : norm_kernel<CLOSE, PF32, 4>;
+  auto k = a.H < 8    ? norm_kernel<CLOSE, PF32, 1, false, false>
+           : a.lg < 6 ? norm_kernel<CLOSE, PF32, 1, false, true>
+           : nv == 1  ? norm_kernel<CLOSE, PF32, 1, true, true>
+           : nv == 2  ? norm_kernel<CLOSE, PF32, 2, true, true>
+                      : norm_kernel<CLOSE, PF32, 4, true, true>;
   return launch_op(k, grid, dim3(threads), s, a);
 }
 

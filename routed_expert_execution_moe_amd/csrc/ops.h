@@ -257,6 +257,20 @@ __device__ inline void op_cols_store(uint8_t* row, bool f32, int64_t c, int n, c
   }
 }
 
+// 8 columns at c but for the first lo (8 and more: none of them)
+__device__ inline void op_cols_store_from(uint8_t* row, bool f32, int64_t c, int lo, const float (&v)[8]) {
+  if (lo <= 0) {
+    op_cols_store(row, f32, c, 8, v);
+  } else {
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i >= lo) {
+        if (f32) ((float*)row)[c + i] = v[i];
+        else ((uint16_t*)row)[c + i] = op_bf16(v[i]);
+      }
+  }
+}
+
 struct OpTile {
   int e, pos0, rows;  // expert, first position, positions (1..BM)
 };

@@ -231,23 +231,52 @@ static hipError_t launch_small_as(const ProductArgs& a, hipStream_t s) {
   return launch_op(product_small_kernel<AT, WT, GLU, MI, NB>, dim3((unsigned)wgs), dim3(kSmWaves * 64), s, a);
 }
 
-// Which variant of an F8 product, by the tiles that a call can make at most and by
-// the mean rows of an expert.
+// Which variant of an F8 product (us on MI355X; "up" and "plain" as below, weights of
+// several calls in rotation):
+//   Big, BF16 rows only, by rounds of the chip: one of Big (256 workgroups) takes about 9/5 of one
+//   of Half (512, two a CU).  Half and Big, N = K = 4096, 2,048, 3,000, 4,096 and 6,000
+//   rows 44, 50; 65, 54; 79, 63; 114, 107 (a tie by the rule); 8192 x 512, 1,300 and
+//   3,000 rows 17.3, 16.4; 27, 29.  Several experts: their last tiles are half
+//   full on average.  8 experts of 256 rows, 4096 x 4096 87, 61; 16 of 256 rows,
+//   GLU 2816 x 1024 31, 43.  Many tiles make no rounds, and Big's short tiles cost
+//   only the rows they have: from 1,024 tiles and 128 mean rows always Big.  Up at 64, 128 and
+//   256 rows 114, 128; 141, 134; 204, 171; plain at 128 and 256 93, 96; 147, 133.
+//   Half, not Shared, from 257 tiles, and with several experts from 128 mean rows.
+//   One expert 4096 x 4096, 1,024 and 2,048 rows 31, 26; 44, 48; FP32 rows 48, 45; 72, 83.
+//   Up at 64 and 128 rows 114, 108; 141, 150; FP32 148, 148; 190, 213.
+//   One expert's few rows stay with the small variant up to a workgroup of 32 x 32 per CU:
+//   small and Shared, 4096 x 4096 at 16, 64 and 128 rows 8.4, 15.9; 13.9, 16.6; 23, 16.5;
+//   2040 x 2080 at 128 and 256 rows 7.8, 11.4; 10.7, 11.6; 8192 x 2048 at 32 and 64
+//   9.2, 10.5; 14.0, 10.8.  FP32 rows, whose tiles expand both operands: up to two, and
+//   up to one of 64 x 64: 4096 x 4096 at 128 and 256 rows 23.5, 27.0; 27.9, 27.8; 2040 x
+//   2080 at 333 and 512 15.2, 18.2; 15.7, 18.7; 8192 x 2048 at 128 19.0, 17.4.
+//   Several experts' up to 127 tiles (one token up 12.7, 14.0; two 16.5, 14.8), FP32 up to 256
+//   (one token of 4096 x 2048 over 256 experts 19.0, 19.4; two 33, 27), FP32 with
+//   GLU below 4 mean rows (up at 2, 4 and 8 rows 53, 59; 679, 645 for 4096 x 4096 over 256; 97, 86).
 static ProductVariant choose_f8(const ProductArgs& a, bool glu) {
   const int64_t n_out = glu ? a.N / 2 : a.N, rows = a.n_rows / a.n_experts;
-  auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * ((n_out + n - 1) / n); };
+  const int groups = std::min(a.n_experts, a.n_rows), g = glu ? 2 : 1;
+  const bool one = a.n_experts == 1;
+  auto wide = [&](int n) { return (n_out + n - 1) / n; };
+  auto tiles = [&](int m, int n) { return op_max_tiles(a, m) * wide(n); };
+  auto rounds = [&](int m, int n, int at_once) {
+    const int64_t t = one ? tiles(m, n) : (a.n_rows / m + groups / 2) * wide(n);
+    return (t + at_once - 1) / at_once;
+  };
   // the tile kernels address the rows of x of a tile with 32-bit offsets
   if (a.x_ld < (1 << 23)) {
-    const int g = glu ? 2 : 1;
-    if (!a.y_f32 && tiles(256, 256 / g) >= 128 && rows >= 128) return ProductVariant::kBig;
-    if (tiles(128, 128 / g) > 256 && rows >= 64) return ProductVariant::kHalf;
-    if (tiles(64, 128 / g) >= 64 && a.n_rows > 8) return ProductVariant::kShared;
+    if (one || rows >= 128) {
+      if (!a.y_f32 && ((!one && tiles(256, 256 / g) >= 1024) || 5 * rounds(128, 128 / g, 512) >= 9 * rounds(256, 256 / g, 256)))
+        return ProductVariant::kBig;
+      if (tiles(128, 128 / g) > 256) return ProductVariant::kHalf;
+    }
+    const bool few = one ? a.n_rows <= 16 || tiles(32, 32) <= (a.y_f32 ? 512 : 256) || (a.y_f32 && tiles(64, 64) <= 256)
+                         : a.y_f32 && glu ? rows < 4 : tiles(64, 128 / g) < (a.y_f32 ? 257 : 128);
+    if (!few) return ProductVariant::kShared;
   }
-  const int groups = std::min(a.n_experts, a.n_rows);
   const int avg = (a.n_rows + groups - 1) / groups;
   if (avg <= 16 || tiles(16, 16) <= 512) return ProductVariant::kSmall16;
-  if (avg <= 64 || tiles(32, 16) <= 512) return ProductVariant::kSmall32;
-  return ProductVariant::kSmall64;
+  return avg <= 64 || tiles(32, 32) <= 512 ? ProductVariant::kSmall32 : ProductVariant::kSmall64;
 }
 
 // Which variant, by the tiles that a call can make at most and by the mean rows
@@ -350,7 +379,6 @@ hipError_t launch_product(const ProductArgs& a, int x_dtype, int w_dtype, bool g
 }
 
 static ProductVariant product_variant(const ProductArgs& a, int x_dtype, int w_dtype, bool glu) {
-  if (x_dtype == MOE_F8) return choose<MOE_F8, MOE_F8>(a, glu);
   if (x_dtype == MOE_MXFP4) return choose<MOE_MXFP4, MOE_MXFP4>(a, glu);
   return w_dtype == MOE_MXFP4 ? choose<MOE_BF16, MOE_MXFP4>(a, glu) : choose<MOE_BF16, MOE_BF16>(a, glu);
 }
@@ -362,10 +390,23 @@ static ProductVariant product_variant(const ProductArgs& a, int x_dtype, int w_d
 extern "C" int moert_product_variant(int x_dtype, int w_dtype, int glu, int n_experts, int n_rows, int N, int K) {
   if (n_experts < 1 || n_rows < 1 || N < 1 || K < 1) return -1;
   moert::ProductArgs a{};
-  a.x_ld = x_dtype == MOE_F8 ? K : x_dtype == MOE_MXFP4 ? K / 2 : (int64_t)K * 2;
+  a.x_ld = x_dtype == MOE_MXFP4 ? K / 2 : (int64_t)K * 2;
   a.n_experts = n_experts;
   a.n_rows = n_rows;
   a.N = N;
   a.K = K;
   return (int)moert::product_variant(a, x_dtype, w_dtype, glu != 0);
+}
+
+// The same for F8, whose choice goes by the type of y too.
+extern "C" int moert_f8_variant(int y_f32, int glu, int n_experts, int n_rows, int N, int K) {
+  if (n_experts < 1 || n_rows < 1 || N < 1 || K < 1) return -1;
+  moert::ProductArgs a{};
+  a.x_ld = K;
+  a.n_experts = n_experts;
+  a.n_rows = n_rows;
+  a.N = N;
+  a.K = K;
+  a.y_f32 = y_f32;
+  return (int)moert::choose_f8(a, glu != 0);
 }

@@ -33,13 +33,13 @@
 namespace moert {
 
 struct F8Big {
-  static constexpr int WavesM = 2, WavesN = 4, MaxI = 8, NJ = 4, PerCu = 1;
+  static constexpr int WavesM = 2, WavesN = 4, MaxI = 8, NJ = 4, Stages = 2, PerCu = 1;
 };
 struct F8Half {
-  static constexpr int WavesM = 2, WavesN = 2, MaxI = 4, NJ = 4, PerCu = 2;
+  static constexpr int WavesM = 2, WavesN = 2, MaxI = 4, NJ = 4, Stages = 2, PerCu = 2;
 };
 struct F8Mid {
-  static constexpr int WavesM = 2, WavesN = 2, MaxI = 2, NJ = 4, PerCu = 2;
+  static constexpr int WavesM = 2, WavesN = 2, MaxI = 2, NJ = 4, Stages = 3, PerCu = 2;
 };
 
 template <class C, bool GLU>
@@ -51,15 +51,16 @@ struct F8Shape {
   static constexpr int WaveParts = GLU ? 2 : 1;        // of those a wave's
   static constexpr int BLoads = StageB / (Waves * 1024);  // copies of a wave and step
   static constexpr int Chunk = 4;                      // steps whose scales come at once
+  static_assert(C::Stages <= Chunk + 1, "a chunk's copies are older than the newest Stages - 2 steps' at its first use");
 };
 
 template <bool GLU, class C, bool Exact>
 __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_f8_kernel(ProductArgs a) {
   using S = F8Shape<C, GLU>;
   using std::integral_constant;
-  constexpr int NJ = C::NJ, NT = GLU ? S::N / 2 : S::N;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_st[2 * S::Stage];
-  __shared__ float s_sc[2][S::Chunk][S::Parts][S::M];
+  constexpr int NJ = C::NJ, NT = GLU ? S::N / 2 : S::N, Stages = C::Stages;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_st[Stages * S::Stage];
+  __shared__ __attribute__((aligned(16))) float s_xs[2][S::M][S::Chunk], s_ws[2][S::Parts][S::Chunk];
   __shared__ int32_t s_y[S::M];  // row of y per tile row, -1 = none
   __shared__ int32_t s_x[S::M];  // row of x (from x0), -1 = none: the product is a row of zeros
 
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
     constexpr int NI = decltype(ni_c)::value;
     constexpr int RowsA = 16 * NI * C::WavesM;
     constexpr int ALoads = (RowsA + S::Waves * 8 - 1) / (S::Waves * 8);  // a wave copies 8 rows at once
-    constexpr int Group = ALoads + S::BLoads;
+    constexpr int Group = ALoads + S::BLoads;  // copies of a wave per step
     auto arow = [&](int i) { return (i * C::WavesM + wm) * 16; };  // first tile row of block i
 
     // Copies.  A lane's piece is the same in every row it copies: 8 Waves rows lie
@@ -133,11 +134,16 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
       if (q < ALoads) tile_copy16(x0 + (int64_t)kt * kTileRow, a_off[q], tile_lds(st_a(buf) + (q * S::Waves + wave) * 1024));
       else tile_copy16(w0 + (int64_t)kt * kTileRow, b_off[q - ALoads], tile_lds(st_b(buf) + ((q - ALoads) * S::Waves + wave) * 1024));
     };
-    auto issue = [&](int kt, int buf) {
-      if (kt < whole || kt * kTileRow + piece * 16 < K) {
+    auto copy_some = [&](int kt, int buf, int from, int to) {
 #pragma unroll
-        for (int q = 0; q < Group; ++q) copy(kt, buf, q);
-      } else {  // the last step's pieces past the row's end become zeros
+      for (int q = 0; q < Group; ++q)
+        if (q >= from && q < to) copy(kt, buf, q);
+    };
+    // the last step, which ends inside: pieces past the row's end become zeros
+    auto copy_end = [&](int kt, int buf) {
+      if (kt * kTileRow + piece * 16 < K) {
+        copy_some(kt, buf, 0, Group);
+      } else {
         const op_u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
         for (int q = 0; q < ALoads; ++q) *(op_u32x4*)(st_a(buf) + (q * S::Waves + wave) * 1024 + lane * 16) = zero;
@@ -145,37 +151,41 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
         for (int q = 0; q < S::BLoads; ++q) *(op_u32x4*)(st_b(buf) + (q * S::Waves + wave) * 1024 + lane * 16) = zero;
       }
     };
+    // A whole step's copies begin in the last row of blocks of the step Stages before
+    // it, when its stage is free, and go on through the first rows of the
+    // next one.
+    constexpr int Head = 4, PerRow = 2;
 
-    // Scales.  A thread makes the products of one row and one row of W's scales.
-    const int sc_row = tid % S::M, sc_part = __builtin_amdgcn_readfirstlane(tid / S::M);
-    const bool sc_mine = sc_part < S::Parts && sc_row < RowsA;
-    const float* const sc_x = xs0 + (int64_t)x_row(sc_row) * KB;
-    const float* const sc_w = ws0 + (int64_t)op_f8_w_block(a, GLU, GLU ? n0 : min(n0 + sc_part * 128, n_out - 1), sc_part) * KB;
-    float sc_v[S::Chunk];
-    auto sc_load = [&](int c) {
-      if (!sc_mine) return;
-      const int b0 = c * S::Chunk;
-      if (b0 + S::Chunk <= KB) {
-        const op_u32x4 v = *(const op_bytes16*)(sc_x + b0), w = *(const op_bytes16*)(sc_w + b0);
-#pragma unroll
-        for (int q = 0; q < S::Chunk; ++q) sc_v[q] = __uint_as_float(v[q]) * __uint_as_float(w[q]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < S::Chunk; ++q) sc_v[q] = sc_x[min(b0 + q, KB - 1)] * sc_w[min(b0 + q, KB - 1)];
-      }
+    // Scales, four steps' at once, copied as they are: a thread a row of x, and in the
+    // next wave a thread a row of W's.  The last chunk begins early enough to end with
+    // the row.  Rows of fewer than four come one by one, before the first step.
+    auto sc_first = [&](int c) { return min(c * S::Chunk, KB - S::Chunk); };
+    const uint32_t sc_off = tid < S::M ? (uint32_t)x_row(tid) * (uint32_t)KB * 4
+                                       : (uint32_t)op_f8_w_block(a, GLU, GLU ? n0 : min(n0 + lane * 128, n_out - 1), min(lane, 1)) * (uint32_t)KB * 4;
+    auto sc_copy = [&](int c) {
+      const int at = sc_first(c);
+      if (wave < (RowsA + 63) / 64) tile_copy16(xs0 + at, sc_off, tile_lds(&s_xs[c & 1][wave * 64][0]));
+      else if (wave == S::M / 64 && lane < S::Parts) tile_copy16(ws0 + at, sc_off, tile_lds(&s_ws[c & 1][0][0]));
     };
-    auto sc_store = [&](int c) {
-      if (!sc_mine) return;
+    auto sc_few = [&] {
 #pragma unroll
-      for (int q = 0; q < S::Chunk; ++q) s_sc[c & 1][q][sc_part][sc_row] = sc_v[q];
+      for (int q = 0; q < S::Chunk; ++q) {
+        if (tid < RowsA) s_xs[0][tid][q] = (xs0 + min(q, KB - 1))[sc_off / 4];
+        if (wave == S::M / 64 && lane < S::Parts) s_ws[0][lane][q] = (ws0 + min(q, KB - 1))[sc_off / 4];
+      }
     };
     const int my_part = GLU ? 0 : wn * 16 * NJ / 128;
     float sc[S::WaveParts][NI];
     auto sc_read = [&](int kt) {
+      const int c = kt / S::Chunk, at = KB < S::Chunk ? kt : kt - sc_first(c);
 #pragma unroll
-      for (int p = 0; p < S::WaveParts; ++p)
+      for (int i = 0; i < NI; ++i) sc[0][i] = s_xs[c & 1][arow(i) + r][at];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) sc[p][i] = s_sc[kt / S::Chunk & 1][kt % S::Chunk][my_part + p][arow(i) + r];
+      for (int p = S::WaveParts - 1; p >= 0; --p) {
+        const float w = s_ws[c & 1][my_part + p][at];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) sc[p][i] = sc[0][i] * w;
+      }
     };
 
     op_f32x4 acc[NI][NJ];
@@ -231,18 +241,24 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
       asm volatile("" : "+v"(acc[i][j]));
     };
 
-    auto step = [&](int kt, int buf) {
-      const bool more = kt + 1 < steps;
+    // One step on stage buf, whose first fragments are in place.  steady: Stages more
+    // whole steps follow, so exactly Stages - 2 steps' copies are newer than the next one's.
+    auto step = [&](int kt, int buf, auto steady_c) {
+      constexpr bool steady = decltype(steady_c)::value;
+      const bool more = steady || kt + 1 < steps;
+      const int next = buf + 1 == Stages ? 0 : buf + 1, before = buf == 0 ? Stages - 1 : buf - 1;
       sc_read(kt);
-      if (kt % S::Chunk == 0 && kt + S::Chunk < steps) sc_load(kt / S::Chunk + 1);
-      if (kt % S::Chunk == 2 && kt - 2 + S::Chunk < steps) sc_store(kt / S::Chunk + 1);
+      if (kt % S::Chunk == 0 && kt + S::Chunk < steps) sc_copy(kt / S::Chunk + 1);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        if (i + 1 < NI) {
+        const bool last = i + 1 == NI;
+        if (!last) {
           read_x(buf, i + 1);
         } else if (more) {
-          tile_sync<0>();
-          read_x(buf ^ 1, 0 + NI);  // NI is even: fragment 0
+          // everyone has read this stage, and the next one is there
+          if (steady) tile_sync<(Stages - 2) * Group>();
+          else tile_sync<0>();
+          read_x(next, NI);  // NI is even: fragment 0
         }
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -253,28 +269,44 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
           }
           part[n % (Late + 1)] = product(j, i);
           if (n >= Late) add(n - Late);
+          if (last && more) read_w(next, j);  // over the fragment that was just used
+          if (steady || kt + Stages - (last ? 0 : 1) < whole) {
+            const int from = last ? 0 : Head + i * PerRow;
+            const int most = last ? Head : i + 2 == NI ? Group : min(from + PerRow, Group);
+            const int at = from + (most - from) * j / NJ, to = from + (most - from) * (j + 1) / NJ;
+            copy_some(kt + Stages - (last ? 0 : 1), last ? buf : before, at, to);
+          }
+          __builtin_amdgcn_sched_barrier(0);  // the order as written
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int n = NI * NJ - Late; n < NI * NJ; ++n) add(n);
-      if (more) {
-        if (kt + 2 < steps) issue(kt + 2, buf);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) read_w(buf ^ 1, j);
-      }
+      if (!steady && kt + Stages == whole && whole < steps) copy_end(whole, buf);
     };
 
-    issue(0, 0);
-    sc_load(0);
-    sc_store(0);
-    if (steps > 1) issue(1, 1);
-    tile_sync<0>();
+    if (KB < S::Chunk) sc_few();
+    else sc_copy(0);
+#pragma unroll
+    for (int kt = 0; kt < Stages; ++kt) {
+      if (kt < whole) copy_some(kt, kt, 0, kt + 1 < Stages ? Group : Head);
+      else if (kt < steps) copy_end(kt, kt);
+    }
+    if (whole >= Stages) tile_sync<(Stages - 2) * Group + Head>();
+    else tile_sync<0>();
     read_x(0, 0);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) read_w(0, j);
+    int kt = 0, buf = 0;
 #pragma unroll 1
-    for (int kt = 0; kt < steps; ++kt) step(kt, kt & 1);
+    for (; kt + Stages < whole; ++kt) {
+      step(kt, buf, std::true_type{});
+      buf = buf + 1 == Stages ? 0 : buf + 1;
+    }
+#pragma unroll 1
+    for (; kt < steps; ++kt) {
+      step(kt, buf, std::false_type{});
+      buf = buf + 1 == Stages ? 0 : buf + 1;
+    }
 
     // Result: a lane's columns are neighbours, 4 NJ of them (with GLU 2 NJ)
     constexpr int CL = GLU ? 2 * NJ : 4 * NJ;
@@ -327,10 +359,9 @@ static hipError_t launch_f8_as(const ProductArgs& a, hipStream_t s) {
 
 template <bool GLU>
 static hipError_t launch_f8(const ProductArgs& a, ProductVariant v, hipStream_t s) {
-  if (a.y_f32)
-    return v == ProductVariant::kHalf ? launch_f8_as<GLU, F8Half, true>(a, s) : launch_f8_as<GLU, F8Mid, true>(a, s);
   if (v == ProductVariant::kBig) return launch_f8_as<GLU, F8Big, false>(a, s);
-  return v == ProductVariant::kHalf ? launch_f8_as<GLU, F8Half, false>(a, s) : launch_f8_as<GLU, F8Mid, false>(a, s);
+  if (v == ProductVariant::kHalf) return a.y_f32 ? launch_f8_as<GLU, F8Half, true>(a, s) : launch_f8_as<GLU, F8Half, false>(a, s);
+  return a.y_f32 ? launch_f8_as<GLU, F8Mid, true>(a, s) : launch_f8_as<GLU, F8Mid, false>(a, s);
 }
 
 hipError_t launch_tile_f8(const ProductArgs& a, bool glu, ProductVariant v, hipStream_t s) {

@@ -262,3 +262,23 @@ def test_oracle_e4m3():
     c, s = OO.f8_quantize(np.array([[448.0] + [0.0] * 15, [np.inf] + [1.0] * 15, [0.0] * 16, [-1e-45] * 16]))
     assert s[0, 0] == 1 and c[0, 0] == 126 and np.isnan(s[1, 0]) and not c[1].any()
     assert s[2, 0] == np.float32(2.0 ** -126) and s[3, 0] == np.float32(2.0 ** -126) and not (c[2:] & 127).any()
+
+
+def test_gpu_sizes_reach_every_f8_variant():
+    """The rule that picks an F8 product's kernel, on the sizes of the GPU tests: every kernel has one."""
+    from tests import test_gpu_f8 as G
+    f = B.lib().moert_f8_variant
+    f.argtypes, f.restype = [ctypes.c_int] * 6, ctypes.c_int
+    names = ["small16", "small32", "small64", "deep", "shared", "half", "big"]
+    assert f(0, 0, 0, 8, 64, 64) == -1
+    got = set()
+    for y_f32 in (0, 1):
+        calls = [(0, 1, M, N, K) for M, N, K in G.GEMM + G.GEMM_TILES]
+        calls += [(glu, E, T * min(k, E), N, K) for T, k, E, N, K in G.GROUPED for glu in (0, 1)]
+        calls += [(int(glu), E, T * k, N, K) for T, k, E, N, K, glu in G.GROUPED_TILES + G.GROUPED_VARIANTS]
+        for glu, *c in calls:
+            n = names[f(y_f32, glu, *c)]
+            got.add((None if n.startswith("small") else y_f32, glu, n))  # the few-row kernels write either type
+    want = {(y, glu, n) for glu in (0, 1) for y, n in [(None, "small16"), (None, "small32"), (None, "small64"), (0, "shared"),
+                                                       (0, "half"), (0, "big"), (1, "shared"), (1, "half")]}
+    assert got == want, (sorted(want - got), sorted(got - want))

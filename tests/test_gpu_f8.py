@@ -185,29 +185,28 @@ class Operand:
         self.v = OO.f8_values(c, s, block_rows)
 
 
-def _eights(v):
-    """v [n, K] as its groups of 8 neighbours of K, [K/8 groups][n, 8]."""
-    return [v[:, i:i + 8] for i in range(0, v.shape[1], 8)]
-
-
 def _cut(x, w):
-    """Sum over groups of 8 of the largest |x w|."""
-    total = np.zeros((len(x), len(w)))
-    for a, b in zip(_eights(np.abs(x)), _eights(np.abs(w))):
-        most = a[:, None, 0] * b[None, :, 0]
-        for i in range(1, a.shape[1]):
-            np.maximum(most, a[:, None, i] * b[None, :, i], out=most)
+    """Sum over groups of 8 neighbours of K of the largest |x w|; x, w on the device."""
+    total = x.new_zeros((len(x), len(w)))
+    a, b = x.abs().t().contiguous(), w.abs().t().contiguous()
+    for k in range(0, len(a), 8):
+        most = a[k][:, None] * b[k]
+        for i in range(k + 1, k + 8):
+            most = most.maximum(a[i][:, None] * b[i])
         total += most
     return total
 
 
 def _bound(x, w, bf16):
-    """Bound of a product's error before its last rounding, and the product."""
-    K = x.shape[1]
-    b = (K + 4) * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T)
+    """The product in fp64 (elementary operations on the device, for speed) and a bound of its error before
+    the last rounding."""
+    import torch
+    x, w = torch.from_numpy(np.ascontiguousarray(x)).cuda(), torch.from_numpy(np.ascontiguousarray(w)).cuda()
+    wt = w.t().contiguous()
+    b = (x.shape[1] + 4) * 2.0 ** -23 * (x.abs() @ wt.abs())
     if bf16:
-        b = b + 7 * 2.0 ** -12 * _cut(x, w)
-    return x @ w.T, b
+        b += 7 * 2.0 ** -12 * _cut(x, w)
+    return (x @ wt).cpu().numpy(), b.cpu().numpy()
 
 
 def _glu(gate, up):
@@ -310,6 +309,11 @@ GROUPED_TILES = [  # T, k, E, N, K, glu
     (2100, 8, 64, 1024, 256, True), (4000, 4, 24, 700, 384, False), (3000, 4, 9, 4096, 144, True),
 ]
 
+GROUPED_VARIANTS = [  # sizes of every other kernel, one expert among them
+    (300, 2, 2, 1300, 272, False), (520, 1, 1, 2100, 272, True), (400, 1, 1, 1100, 272, True), (700, 2, 10, 1000, 656, True),
+    (2600, 2, 8, 2048, 528, True), (900, 1, 1, 2200, 528, False), (80, 4, 16, 700, 272, True),
+]
+
 
 class Experts:
     def __init__(self, t, rng, E, N, K, glu, sigma=0.05):
@@ -368,10 +372,33 @@ def test_grouped(t, B, T, k, E, N, K, glu, out):
 
 
 @pytest.mark.parametrize("out", ["float32", "bfloat16"])
-@pytest.mark.parametrize("T,k,E,N,K,glu", GROUPED_TILES)
+@pytest.mark.parametrize("T,k,E,N,K,glu", GROUPED_TILES + GROUPED_VARIANTS)
 def test_grouped_tiles(t, B, T, k, E, N, K, glu, out):
     log(f"f8 grouped tiles {T}x{k} E{E} {N}x{K} glu={glu} {out}")
     _grouped_case(t, B, T, k, E, N, K, glu, out)
+
+
+@pytest.mark.parametrize("out", ["float32", "bfloat16"])
+@pytest.mark.parametrize("K", [128, 256, 384, 512, 640, 768, 896, 1024, 1040, 1168, 1296, 1424, 2064])
+def test_every_number_of_steps(t, B, K, out):
+    """Whole and ragged steps from fewer than the stages to several chunks of scales, on each tile."""
+    log(f"f8 steps {K} {out}")
+    for M, N in ((300, 1100), (900, 4100), (2300, 4200)):
+        _gemm(t, B, M, N, K, out)
+
+
+@pytest.mark.parametrize("out", ["float32", "bfloat16"])
+def test_rows_far_apart(t, B, out):
+    """Rows of x 2^23 bytes apart and more, which the tiles' 32-bit offsets do not reach."""
+    log(f"f8 rows far apart {out}")
+    rng = np.random.default_rng(11)
+    M, N, K = 300, 1100, 272
+    x, w = Operand(t, rng, M, K, 1), Operand(t, rng, N, K, 128, 0.05)
+    far = t.empty((M, 1 << 23), dtype=t.uint8, device="cuda").view(t.float8_e4m3fn)[:, :K]
+    far.copy_(x.t)
+    y = t.empty((M, N), dtype=getattr(t, out), device="cuda")
+    B.moe_f8_gemm(far, x.scales, w.t, w.scales, y)
+    _close(y, *_bound(x.v, w.v, out == "bfloat16"), out == "bfloat16", "far")
 
 
 @pytest.mark.parametrize("rows", [40, 1500])
