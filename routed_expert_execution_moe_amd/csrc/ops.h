@@ -185,8 +185,10 @@ __device__ inline uint2 op_f8x8(const float (&v)[8], const OpF8Scale& s) {
   return s.bad ? make_uint2(0, 0) : make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-// 16 bytes at an address of any alignment: global memory takes them in one access
+// 16 and 8 bytes at an address of any alignment: global memory takes them in one access
+typedef unsigned int op_u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned int op_bytes16 __attribute__((ext_vector_type(4), aligned(1)));
+typedef unsigned int op_bytes8 __attribute__((ext_vector_type(2), aligned(1)));
 
 // 8 columns of a row in fp32 or bf16, as loaded
 struct OpCols {

@@ -186,40 +186,47 @@ __global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(Product
   }
   if (k0 < K) multiply(load(k0, std::false_type{}));
 
-  // the waves' sums, halved three times: always the same order
+  // The waves' sums meet in LDS, always in the same order: those of waves w and w + 4,
+  // then (0 + 2) + (1 + 3), which every wave adds up for its own blocks and stores.
+  if (wave >= kSmWaves / 2)
 #pragma unroll
-  for (int half = kSmWaves / 2; half; half >>= 1) {
-    if (wave >= half && wave < 2 * half)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int b = 0; b < NW; ++b) s_red[wave - kSmWaves / 2][i * NW + b][lane] = acc[i][b];
+  __syncthreads();
+  if (wave < kSmWaves / 2)
 #pragma unroll
-        for (int b = 0; b < NW; ++b) s_red[wave - half][i * NW + b][lane] = acc[i][b];
-    __syncthreads();
-    if (wave < half)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int i = 0; i < MI; ++i)
+      for (int b = 0; b < NW; ++b) s_red[wave][i * NW + b][lane] = acc[i][b] + s_red[wave][i * NW + b][lane];
+  __syncthreads();
+  auto total = [&](int k) { return (s_red[0][k][lane] + s_red[2][k][lane]) + (s_red[1][k][lane] + s_red[3][k][lane]); };
 #pragma unroll
-        for (int b = 0; b < NW; ++b) acc[i][b] += s_red[wave][i * NW + b][lane];
-    if (half > 1) __syncthreads();
-  }
-  if (wave) return;
+  for (int u = 0; u < MI * NB; ++u) {
+    if (wave != u % kSmWaves) continue;
+    const int i = u / NB, b = u % NB, m = i * 16 + r;
+    op_f32x4 v = total(i * NW + b);
+    if constexpr (GLU) {
+      const op_f32x4 up = total(i * NW + b + NB);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m = i * 16 + r;
+      for (int q = 0; q < 4; ++q) v[q] = op_silu_mul(v[q], up[q]);
+    }
+    if (!live[i]) v = op_f32x4{};
     const int row = m < t.rows ? op_y_row(a, t.pos0 + m) : -1;
-    if (row < 0) continue;
+    const int n = n0 + b * 16 + 4 * g;
+    if (row < 0 || n >= n_out) continue;
+    const int64_t o = (int64_t)row * a.ldy + n;
+    if (n + 4 <= n_out) {
+      if (a.y_f32) *(op_bytes16*)((float*)a.y + o) = __builtin_bit_cast(op_u32x4, v);
+      else *(op_bytes8*)((uint16_t*)a.y + o) = op_u32x2{op_bf16_pair(v[0], v[1]), op_bf16_pair(v[2], v[3])};
+    } else {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + b * 16 + 4 * g + q;
-        if (n >= n_out) continue;
-        const float z = GLU ? op_silu_mul(acc[i][b][q], acc[i][b + NW - NB][q]) : acc[i][b][q];
-        const float v = live[i] ? z : 0.f;
-        const int64_t o = (int64_t)row * a.ldy + n;
-        if (a.y_f32) ((float*)a.y)[o] = v;
-        else ((uint16_t*)a.y)[o] = op_bf16(v);
+      for (int q = 0; q < 3; ++q) {
+        if (n + q >= n_out) continue;
+        if (a.y_f32) ((float*)a.y)[o + q] = v[q];
+        else ((uint16_t*)a.y)[o + q] = op_bf16(v[q]);
       }
+    }
   }
 }
 

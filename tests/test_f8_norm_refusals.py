@@ -242,6 +242,8 @@ def test_binding_refusals():
     _refused(B.moe_combine_norm, p, cw, x, res, gate=torch.zeros(4, 2))
     _refused(B.moe_combine_norm, p, cw, x, res, gate=torch.zeros(144))
     _refused(B.moe_combine_norm, p, cw, x, res, post_weight=wt[:100])
+    _refused(B.moe_combine_norm, p, cw, x, res, scale=1e300)
+    _refused(B.moe_combine_norm, p, cw, x, res, scale="1")
     _refused(B.moe_combine_norm, p, cw, x, res, ids=torch.zeros(4, 2, dtype=torch.int32))
     _refused(B.moe_combine_norm, p, cw, x, res, ids=torch.zeros(4, 2, dtype=torch.int64), n_experts=4)
 
