@@ -198,7 +198,7 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
       uint32_t top = 0;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        r[i][c] = r[i][c] * inv * f[c];
+        r[i][c] = r[i][c] * f[c] * inv;  // bf16 x and weight: the first product is exact
         top = max(top, __float_as_uint(r[i][c]) & 0x7FFFFFFFu);
       }
       if (a.y_dtype != MOE_F8) {

@@ -321,28 +321,37 @@ struct OpTiles {
     total = min(__builtin_amdgcn_readlane(incl, 63), most);
   }
 
-  __device__ inline bool find(const ProductArgs& a, int BM, int t, OpTile* out) const {
+  // The expert of the t-th tile: its number, first position, positions and first tile.
+  __device__ inline bool expert(const ProductArgs& a, int BM, int t, int* e, int* lo_e, int* n_e, int* first) const {
     if (!a.offsets) {
-      out->e = 0;
-      out->pos0 = t * BM;
-      out->rows = min(BM, a.n_rows - out->pos0);
+      *e = *lo_e = *first = 0;
+      *n_e = a.n_rows;
       return t < total;
     }
     const uint64_t past = __ballot(incl > t);
     if (!past) return false;
     const int owner = __builtin_ctzll(past), per = (a.n_experts + 63) >> 6;
-    const int left = t - __builtin_amdgcn_readlane(incl - mine, owner);
-    const int lane = threadIdx.x & 63, e = owner * per + lane;
+    const int begin = __builtin_amdgcn_readlane(incl - mine, owner), left = t - begin;
+    const int lane = threadIdx.x & 63, i = owner * per + lane;
     int lo = 0, n = 0;
-    if (lane < per && e < a.n_experts) n = range(a, e, &lo);
+    if (lane < per && i < a.n_experts) n = range(a, i, &lo);
     const int tiles = (n + BM - 1) / BM, upto = op_scan(tiles);
     const uint64_t hit = __ballot(upto > left);
     if (!hit) return false;  // offsets changed since they were counted
     const int at = __builtin_ctzll(hit);
-    const int skip = (left - __builtin_amdgcn_readlane(upto - tiles, at)) * BM;
-    out->e = owner * per + at;
-    out->pos0 = __builtin_amdgcn_readlane(lo, at) + skip;
-    out->rows = min(BM, __builtin_amdgcn_readlane(n, at) - skip);
+    *e = owner * per + at;
+    *lo_e = __builtin_amdgcn_readlane(lo, at);
+    *n_e = __builtin_amdgcn_readlane(n, at);
+    *first = begin + __builtin_amdgcn_readlane(upto - tiles, at);
+    return true;
+  }
+
+  __device__ inline bool find(const ProductArgs& a, int BM, int t, OpTile* out) const {
+    int lo, n, first;
+    if (!expert(a, BM, t, &out->e, &lo, &n, &first)) return false;
+    const int skip = (t - first) * BM;
+    out->pos0 = lo + skip;
+    out->rows = min(BM, n - skip);
     return true;
   }
 };

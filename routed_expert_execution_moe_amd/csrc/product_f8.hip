@@ -32,50 +32,57 @@
 
 namespace moert {
 
+// Area: bytes of LDS for the stages.  As many stages as fit, three at most: a short
+// tile's products do not cover the latency of its copies, those of 256 rows do.
 struct F8Big {
-  static constexpr int WavesM = 2, WavesN = 4, MaxI = 8, NJ = 4, Stages = 2, PerCu = 1;
+  static constexpr int WavesM = 2, WavesN = 4, MaxI = 8, NJ = 4, Area = 144 << 10, PerCu = 1;
 };
 struct F8Half {
-  static constexpr int WavesM = 2, WavesN = 2, MaxI = 4, NJ = 4, Stages = 2, PerCu = 2;
+  static constexpr int WavesM = 2, WavesN = 2, MaxI = 4, NJ = 4, Area = 72 << 10, PerCu = 2;
 };
 struct F8Mid {
-  static constexpr int WavesM = 2, WavesN = 2, MaxI = 2, NJ = 4, Stages = 3, PerCu = 2;
+  static constexpr int WavesM = 2, WavesN = 2, MaxI = 2, NJ = 4, Area = 72 << 10, PerCu = 2;
 };
 
 template <class C, bool GLU>
 struct F8Shape {
   static constexpr int Waves = C::WavesM * C::WavesN, Threads = Waves * 64;
   static constexpr int M = 16 * C::MaxI * C::WavesM, N = 16 * C::NJ * C::WavesN;
-  static constexpr int StageA = M * kTileRow, StageB = N * kTileRow, Stage = StageA + StageB;
+  static constexpr int StageB = N * kTileRow;
   static constexpr int Parts = GLU ? 2 : N / 128;      // scale rows of W in a tile
   static constexpr int WaveParts = GLU ? 2 : 1;        // of those a wave's
   static constexpr int BLoads = StageB / (Waves * 1024);  // copies of a wave and step
   static constexpr int Chunk = 4;                      // steps whose scales come at once
-  static_assert(C::Stages <= Chunk + 1, "a chunk's copies are older than the newest Stages - 2 steps' at its first use");
 };
 
 template <bool GLU, class C, bool Exact>
 __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_f8_kernel(ProductArgs a) {
   using S = F8Shape<C, GLU>;
   using std::integral_constant;
-  constexpr int NJ = C::NJ, NT = GLU ? S::N / 2 : S::N, Stages = C::Stages;
-  __shared__ __attribute__((aligned(1024))) uint8_t s_st[Stages * S::Stage];
+  constexpr int NJ = C::NJ, NT = GLU ? S::N / 2 : S::N;
+  __shared__ __attribute__((aligned(1024))) uint8_t s_st[C::Area];
   __shared__ __attribute__((aligned(16))) float s_xs[2][S::M][S::Chunk], s_ws[2][S::Parts][S::Chunk];
   __shared__ int32_t s_y[S::M];  // row of y per tile row, -1 = none
   __shared__ int32_t s_x[S::M];  // row of x (from x0), -1 = none: the product is a row of zeros
 
   const int n_out = GLU ? a.N / 2 : a.N;
   const int n_ntiles = (n_out + NT - 1) / NT;
-  // XCD-aware order, as in product_tile.h
+  // XCD-aware order, as in product_tile.h: XCD i takes the i-th eighth of a list.
+  // It goes by expert, then by groups of six of its M-tiles, then by N-tile: a
+  // group that mixed experts would bring the W of those that it cuts twice.
   const OpTiles tiles(a, S::M);
-  const int per_xcd = (tiles.total * n_ntiles + 7) >> 3;
+  const int per_xcd = (tiles.total * n_ntiles + 7) >> 3;  // the launch keeps this below 2^31
   const int local = blockIdx.x >> 3, f = (blockIdx.x & 7) * per_xcd + local;
   if (local >= per_xcd || f >= tiles.total * n_ntiles) return;
-  const int grp = f / (4 * n_ntiles), rem = f - grp * 4 * n_ntiles;
-  const int in_grp = min(4, tiles.total - grp * 4);
-  const int nt = rem / in_grp;
   OpTile t;
-  if (!tiles.find(a, S::M, grp * 4 + rem - nt * in_grp, &t)) return;
+  int lo, n, first;
+  if (!tiles.expert(a, S::M, f / n_ntiles, &t.e, &lo, &n, &first)) return;
+  constexpr int MGroup = 6;
+  const int in_expert = f - first * n_ntiles, grp = in_expert / (MGroup * n_ntiles);
+  const int rem = in_expert - grp * MGroup * n_ntiles, in_grp = min(MGroup, (n + S::M - 1) / S::M - grp * MGroup);
+  const int nt = rem / in_grp, skip = (grp * MGroup + rem - nt * in_grp) * S::M;
+  t.pos0 = lo + skip;
+  t.rows = min(S::M, n - skip);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -113,6 +120,9 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
   auto run = [&](auto ni_c) {
     constexpr int NI = decltype(ni_c)::value;
     constexpr int RowsA = 16 * NI * C::WavesM;
+    constexpr int StageA = RowsA * kTileRow, Stage = StageA + S::StageB;
+    constexpr int Stages = C::Area / Stage < 3 ? C::Area / Stage : 3;
+    static_assert(Stages >= 2 && Stages <= S::Chunk + 1, "a chunk's copies are older than the newest Stages - 2 steps' at its first use");
     constexpr int ALoads = (RowsA + S::Waves * 8 - 1) / (S::Waves * 8);  // a wave copies 8 rows at once
     constexpr int Group = ALoads + S::BLoads;  // copies of a wave per step
     auto arow = [&](int i) { return (i * C::WavesM + wm) * 16; };  // first tile row of block i
@@ -128,8 +138,8 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
 #pragma unroll
     for (int q = 0; q < S::BLoads; ++q)
       b_off[q] = (uint32_t)w_row((q * S::Waves + wave) * 8 + cr) * (uint32_t)K + piece * 16;
-    auto st_a = [&](int buf) { return s_st + buf * S::Stage; };
-    auto st_b = [&](int buf) { return s_st + buf * S::Stage + S::StageA; };
+    auto st_a = [&](int buf) { return s_st + buf * Stage; };
+    auto st_b = [&](int buf) { return s_st + buf * Stage + StageA; };
     auto copy = [&](int kt, int buf, int q) {
       if (q < ALoads) tile_copy16(x0 + (int64_t)kt * kTileRow, a_off[q], tile_lds(st_a(buf) + (q * S::Waves + wave) * 1024));
       else tile_copy16(w0 + (int64_t)kt * kTileRow, b_off[q - ALoads], tile_lds(st_b(buf) + ((q - ALoads) * S::Waves + wave) * 1024));
@@ -200,14 +210,14 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
     // a lane's place in 16 rows, for each of its two pieces; whole blocks of 16 rows
     // leave the swizzle's key as it is
     const uint32_t at0 = tile_at(r, g), at1 = tile_at(r, 4 + g);
-    const uint32_t xa = wm * 16 * kTileRow, wa = S::StageA + wn * NJ * 16 * kTileRow;
+    const uint32_t xa = wm * 16 * kTileRow, wa = StageA + wn * NJ * 16 * kTileRow;
     auto read_x = [&](int buf, int i) {
-      const uint8_t* p = s_st + buf * S::Stage + xa + (i % NI) * C::WavesM * 16 * kTileRow;
+      const uint8_t* p = s_st + buf * Stage + xa + (i % NI) * C::WavesM * 16 * kTileRow;
       xf[i & 1][0] = *(const op_u32x4*)(p + at0);
       xf[i & 1][1] = *(const op_u32x4*)(p + at1);
     };
     auto read_w = [&](int buf, int j) {
-      const uint8_t* p = s_st + buf * S::Stage + wa + j * 16 * kTileRow;
+      const uint8_t* p = s_st + buf * Stage + wa + j * 16 * kTileRow;
       wf[j][0] = *(const op_u32x4*)(p + at0);
       wf[j][1] = *(const op_u32x4*)(p + at1);
     };
