@@ -10,8 +10,8 @@
 // registers: 16 neighbouring lanes hold a block of 128 columns.
 //
 // HBM bounds both: 8192 tokens of 8 fp32 rows of 4,096, normed, gated, added and normed again,
-// 238 us, 5.3 TB/s (a plain copy reaches 5.2); norm of 8192 x 4096 bf16 to F8 25.0 us,
-// 4.1 TB/s, whose rows are too short a work for a workgroup to hide its own start.
+// 237 us, 5.3 TB/s (a plain copy reaches 5.2); norm of 32768 x 4096 bf16 to F8 80 us,
+// 5.0 TB/s, of 8192 x 4096 23.5, 4.3 TB/s with the start and end of a short launch.
 #include "ops.h"
 
 namespace moert {
@@ -51,7 +51,7 @@ __device__ inline float norm_sum(float v, int lg, float* red) {
 template <bool CLOSE, bool PF32, int NV, bool UNI, bool WIDE>
 __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
   constexpr int PB = PF32 ? 4 : 2;
-  constexpr bool Early = NV == 1;  // weights and gate are requested with the row: one latency
+  constexpr bool Early = !CLOSE || NV == 1;  // weights and gate are requested with the row: one latency
   __shared__ float s_red[2][kNormMost / 64];
   const bool own = UNI && a.lg >= 7;  // the workgroup's one row
   const int G = own ? (int)blockDim.x : 1 << a.lg;
@@ -102,18 +102,25 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
     else op_cols_store(row, f32, col[i], H - col[i], v);
   };
 
-  for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.T; row0 += (int64_t)gridDim.x * per) {
+  OpCols weight[NV], x[NV];  // x: the row to come, requested while its predecessor is at work
+  if (Early && a.weight)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) weight[i] = load(a.weight, a.weight_f32, i);
+  auto request = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = load(a.p + (row < a.T ? row : 0) * a.ldp * PB, PF32, i);
+  };
+  const int64_t first = (int64_t)blockIdx.x * per, step = (int64_t)gridDim.x * per;
+  if (!CLOSE) request(first + sub);
+  for (int64_t row0 = first; row0 < a.T; row0 += step) {
     const int64_t row = row0 + sub;
     const bool live = row < a.T;  // lanes without a row go along, for the barriers
     const int64_t at = live ? row : 0;
     float r[NV][8];
-    OpCols weight[NV];
-    if (Early && a.weight)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) weight[i] = load(a.weight, a.weight_f32, i);
     if constexpr (!CLOSE) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) op_cols_get(load(a.p + at * a.ldp * PB, PF32, i), PF32, r[i]);
+      for (int i = 0; i < NV; ++i) op_cols_get(x[i], PF32, r[i]);
+      if (row0 + step < a.T) request(row + step);
     } else {
       const uint8_t* const gate = a.gate ? a.gate + at * a.ldg * (a.gate_f32 ? 4 : 2) : nullptr;
       OpCols res[NV], post[NV], gates[NV];
@@ -219,9 +226,9 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
 template <bool CLOSE, bool PF32>
 static hipError_t norm_typed(NormArgs& a, hipStream_t s) {
   // Two pieces a thread from 1,024 columns on, four past 8,192: fewer waves wait at a
-  // row's barriers.  One and two pieces: norm 8192 x 4096 bf16 to F8 31.5 and 25.0 us, end of
-  // a block 8192 x 2 x 2048 bf16 54 and 44 (four: norm 27.0); two and four: norm 4096
-  // x 16384 64.6 and 56.5.  fp32 rows, which bring twice the bytes a column, one
+  // row's barriers.  One, two and four pieces: norm 8192 x 4096 bf16 to F8 27.5, 23.4,
+  // 26.2 us, 4096 x 16384 two and four 50.4, 47.9; end of a block 8192 x 2 x 2048 bf16
+  // one and two 54, 44.  Its fp32 rows, which bring twice the bytes a column, one
   // piece up to 4,096 columns: 8192 x 8 x 4096 238 and 248.
   const int pieces = (a.H + 7) / 8;
   int threads = kNormShared, nv = 1;
@@ -233,7 +240,12 @@ static hipError_t norm_typed(NormArgs& a, hipStream_t s) {
     a.lg = 10;
   }
   const int64_t per = a.lg < 7 ? threads >> a.lg : 1;
-  const dim3 grid((unsigned)std::min<int64_t>((a.T + per - 1) / per, 1 << 20));
+  // Norms of several rows a workgroup, the next one's loads and the weights in hand:
+  // twice the threads that the chip holds.  As many, twice as many and one row each:
+  // 32768 x 4096 bf16 to F8 88, 80, 88 us, 65536 x 512 27.0, 24.0, 27.0 (each row's
+  // weights anew, nothing ahead: 102 and 25).
+  const int64_t most = CLOSE ? 1 << 20 : 2 * 256 * 2048 / threads;
+  const dim3 grid((unsigned)std::min<int64_t>((a.T + per - 1) / per, most));
   auto k = a.H < 8    ? norm_kernel<CLOSE, PF32, 1, false, false>
            : a.lg < 6 ? norm_kernel<CLOSE, PF32, 1, false, true>
            : nv == 1  ? norm_kernel<CLOSE, PF32, 1, true, true>
