@@ -423,7 +423,7 @@ def moe_mx_dequantize(codes, scales, y, stream=None):
 
 def _rows_operand(me, x, x_scales):
     """(rows, K, dtype, ldx) of x: bf16 rows, or codes with their scales."""
-    if x.__class__ is torch.Tensor and x.dtype is torch.float8_e4m3fn:
+    if isinstance(x, torch.Tensor) and x.dtype is torch.float8_e4m3fn:
         R, K, ld = _matrix(me, "x", x, _F8)
         _need(x_scales is not None, me, "x in 8 bits needs x_scales")
         _whole(me, "x_scales", x_scales, _F32, (R, -(-K // 128)))

@@ -140,6 +140,18 @@ def test_quantize_several_matrices(t, B):
             assert np.array_equal(_np(y[i]), OO.f8_values(c, s, 128).astype(np.float32))
 
 
+def test_more_matrices_than_a_grid_dimension(t, B):
+    log("f8 quantize many matrices")
+    x = t.arange(2500, device="cuda").remainder(17).add(1).float()[:, None, None].expand(2500, 3, 16).contiguous()
+    codes = t.empty((2500, 3, 16), dtype=t.float8_e4m3fn, device="cuda")
+    scales = t.empty((2500, 1, 1), device="cuda")
+    B.moe_f8_quantize(x, codes, scales, block_rows=128)
+    assert bool((codes.float() == 448).all()) and t.equal(scales.view(-1), (x[:, 0, 0].double() / 448).float())
+    y = t.empty_like(x)
+    B.moe_f8_dequantize(codes, scales, y, block_rows=128)
+    assert bool(((y - x).abs() <= x * 2.0 ** -23).all())
+
+
 @pytest.mark.parametrize("block_rows", [1, 128])
 def test_quantize_past_32_bits(t, B, block_rows):
     """More than 2^32 bytes of x, codes and y; more blocks than one step of the walk."""
@@ -478,6 +490,24 @@ def test_gemm_weights_near_the_32_bit_end(t, B):
             assert bool((y[:, hit] == 2).all())
             y[:, hit] = 0
             assert bool((y == 0).all())
+
+
+def test_parameters_and_another_stream(t, B):
+    """Operands that are parameters of a module; a stream of its own without a current one."""
+    log("f8 parameters")
+    rng = np.random.default_rng(14)
+    M, N, K = 200, 300, 272
+    x, w = Operand(t, rng, M, K, 1), Operand(t, rng, N, K, 128, 0.05)
+    p = lambda v: t.nn.Parameter(v, requires_grad=False)  # noqa: E731
+    a, b, c = (t.empty((M, N), device="cuda") for _ in range(3))
+    B.moe_f8_gemm(x.t, x.scales, w.t, w.scales, a)
+    s = t.cuda.Stream()
+    s.wait_stream(t.cuda.current_stream())
+    B.moe_f8_gemm(p(x.t), p(x.scales), p(w.t), p(w.scales), b, stream=s)
+    off = _dev(t, np.array([0, M], np.int32))
+    B.moe_grouped_gemm(p(x.t), p(w.t[None]), off, c, x_scales=p(x.scales), w_scales=p(w.scales[None]), stream=s.cuda_stream)
+    t.cuda.synchronize()
+    assert t.equal(a, b) and t.equal(a, c)
 
 
 def test_products_repeat_bit_for_bit(t, B):
