@@ -23,15 +23,14 @@
 //                   to bf16, which is exact: the 8-bit matrix instructions keep
 //                   13 bits of each product, and loads bound here
 //
-// One token against 4096 x 4096 in MXFP4 (8.9 MB) takes 5.6 us of kernel and
-// eight tokens of the same 7.6; 64 x 4096 x 4096 takes 15.2 us in 32 x 32 blocks.
-// Clocks of a workgroup (medians): one token of the above: 1,100 to find its tile,
-// 250 for its rows, 6,800 for a wave's four turns, 1,100 for the sums and 1,000 for
-// the store; 333 x 2040 x 2080 in 64 x 64 blocks (15.5 us): 900, 500, 17,200 for
-// three turns, 4,600 and 9,000, since one wave stores the whole block.  What bounds
-// the turns past a few rows is their loads: fragments come through the vector
-// cache once per wave, (MI + NB) of them per MI*NB products, and with W in 4 bits
-// each of x is four times one of W.
+// One token against 4096 x 4096 in MXFP4 (8.9 MB) takes 5.6 us of kernel, in F8 (16.8 MB)
+// 5.4, and eight tokens in MXFP4 7.6; 64 x 4096 x 4096 takes 15 us in 32 x 32 blocks, F8
+// 12.0.  Of one token's 10,200 clocks in MXFP4 1,100 find the tile, 250 its rows, 6,800
+// are a wave's four turns.  333 x 2040 x 2080 in 64 x 64 blocks takes 12.6 us, F8 11.2 (15.9
+// and 14.4 when the sums were halved three times and one wave stored the whole
+// block).  What bounds the turns past a few rows is their loads: fragments come
+// through the vector cache once per wave, (MI + NB) of them per MI*NB products, and
+// with W in 4 bits each of x is four times one of W.
 #include <type_traits>
 
 #include "ops.h"
@@ -287,7 +286,7 @@ static ProductVariant choose_f8(const ProductArgs& a, bool glu) {
 }
 
 // Which variant, by the tiles that a call can make at most and by the mean rows
-// of an expert (us on MI355X; "up" is a GLU product of N = 1536, K = 2048 over 128
+// of an expert (us on MI355X, the small variant's before every wave stored its blocks; "up" is a GLU product of N = 1536, K = 2048 over 128
 // experts, "plain" one without GLU of N = 2048, K = 768, both with 8 experts a
 // token):
 //   Mid, not the small variant, from 64 tiles (W4, whose small variant is the
