@@ -24,7 +24,7 @@
 //                   13 bits of each product, and loads bound here
 //
 // One token against 4096 x 4096 in MXFP4 (8.9 MB) takes 5.6 us of kernel, in F8 (16.8 MB)
-// 5.4, and eight tokens in MXFP4 7.6; 64 x 4096 x 4096 takes 15 us in 32 x 32 blocks, F8
+// 5.4, and a call for eight in MXFP4 6.8; 64 x 4096 x 4096 takes 13.7 us in 32 x 32 blocks, F8
 // 12.0.  Of one token's 10,200 clocks in MXFP4 1,100 find the tile, 250 its rows, 6,800
 // are a wave's four turns.  333 x 2040 x 2080 in 64 x 64 blocks takes 12.6 us, F8 11.2 (15.9
 // and 14.4 when the sums were halved three times and one wave stored the whole
@@ -286,9 +286,9 @@ static ProductVariant choose_f8(const ProductArgs& a, bool glu) {
 }
 
 // Which variant, by the tiles that a call can make at most and by the mean rows
-// of an expert (us on MI355X, the small variant's before every wave stored its blocks; "up" is a GLU product of N = 1536, K = 2048 over 128
-// experts, "plain" one without GLU of N = 2048, K = 768, both with 8 experts a
-// token):
+// of an expert (us on MI355X, the small variant's before all of its waves stored;
+// "up" is a GLU product of N = 1536, K = 2048 over 128 experts, "plain" one without
+// GLU of N = 2048, K = 768, both with 8 experts a token):
 //   Mid, not the small variant, from 64 tiles (W4, whose small variant is the
 //   faster: 129).  W4A4 4096x4096 at 64 and 128 rows 11.8 small, 12.6 Mid and
 //   16.8, 12.5; bf16 at 128 and 256 rows 29.5, 32.1 and 38.7, 31.9; W4 at 128, 512
