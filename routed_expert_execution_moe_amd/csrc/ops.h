@@ -292,28 +292,41 @@ __device__ inline int op_scan(int v) {
 // The BM-row tiles of all groups, expert by expert.  One wave on its own: lane
 // l counts the tiles of its E/64 experts and a wave scan orders them; every
 // lane then gets the total, and find() the t-th tile: the lane that holds it,
-// then, its experts (at most 16) a lane each, the expert.  Offsets are clamped
+// then the expert.  Up to 256 experts a lane's offsets are loaded at once and stay in
+// registers (clocks to the tile's expert 4,000 -> 3,400 with 128, F8 down of 512 tokens
+// over 256 experts 103 -> 95 us); past that they are read again, its experts (at
+// most 16) a lane each.  Offsets are clamped
 // into 0..n_rows and the counts to what ascending ones can make (the launch
 // keeps that below 2^24, so no sum overflows): bad offsets cost results but
 // no access out of range.
 struct OpTiles {
+  static constexpr int Few = 4;  // experts of a lane whose offsets stay in registers
   int incl, mine, total;
+  int off[Few + 1];
 
   static __device__ inline int range(const ProductArgs& a, int e, int* lo) {
     *lo = min(max(a.offsets[e], 0), a.n_rows);
     return max(min(max(a.offsets[e + 1], 0), a.n_rows) - *lo, 0);
   }
 
-  __device__ inline OpTiles(const ProductArgs& a, int BM) : incl(0), mine(0) {
+  __device__ inline OpTiles(const ProductArgs& a, int BM) : incl(0), mine(0), off{} {
     if (!a.offsets) {
       total = (a.n_rows + BM - 1) / BM;
       return;
     }
     const int lane = threadIdx.x & 63, per = (a.n_experts + 63) >> 6;
-    for (int i = 0; i < per; ++i) {
-      const int e = lane * per + i;
-      int lo;
-      if (e < a.n_experts) mine += (range(a, e, &lo) + BM - 1) / BM;
+    if (per <= Few) {
+#pragma unroll
+      for (int i = 0; i <= Few; ++i)
+        off[i] = min(max(a.offsets[min(lane * per + min(i, per), a.n_experts)], 0), a.n_rows);
+#pragma unroll
+      for (int i = 0; i < Few; ++i) mine += (max(off[i + 1] - off[i], 0) + BM - 1) / BM;
+    } else {
+      for (int i = 0; i < per; ++i) {
+        const int e = lane * per + i;
+        int lo;
+        if (e < a.n_experts) mine += (range(a, e, &lo) + BM - 1) / BM;
+      }
     }
     const int most = a.n_rows / BM + min(a.n_experts, a.n_rows);
     mine = min(mine, most);
@@ -332,6 +345,24 @@ struct OpTiles {
     if (!past) return false;
     const int owner = __builtin_ctzll(past), per = (a.n_experts + 63) >> 6;
     const int begin = __builtin_amdgcn_readlane(incl - mine, owner), left = t - begin;
+    if (per <= Few) {
+      int upto = 0;
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < Few; ++i) {
+        const int lo = __builtin_amdgcn_readlane(off[i], owner);
+        const int n = max(__builtin_amdgcn_readlane(off[i + 1], owner) - lo, 0), tiles = (n + BM - 1) / BM;
+        if (!found && upto + tiles > left) {
+          *e = owner * per + i;
+          *lo_e = lo;
+          *n_e = n;
+          *first = begin + upto;
+          found = true;
+        }
+        upto += tiles;
+      }
+      return found;
+    }
     const int lane = threadIdx.x & 63, i = owner * per + lane;
     int lo = 0, n = 0;
     if (lane < per && i < a.n_experts) n = range(a, i, &lo);

@@ -451,6 +451,30 @@ def test_grouped_bad_indices_and_offsets(t, B, rows):
     assert bool((guard[0] == 7).all()) and bool((guard[-1] == 7).all())
 
 
+@pytest.mark.parametrize("E", [1, 2, 63, 64, 65, 128, 129, 192, 255, 256, 257, 320, 1000, 1024])
+def test_every_count_of_experts(t, B, E):
+    """The tile's expert among one to sixteen of a lane, with experts of no rows at the start, the end and between."""
+    log(f"f8 experts {E}")
+    rng = np.random.default_rng(E)
+    N, K = 256, 128
+    W = Operand(t, rng, E * N, K, 128, 0.05)
+    wt, ws = W.t.view(E, N, K), W.scales.view(E, N // 128, 1)
+    for rows in (300, 20000):
+        full = rng.random(E) < 0.6
+        full[rng.integers(E)] = True
+        if E > 2:
+            full[0] = full[-1] = False
+            full[E // 2] = True
+        n = rng.multinomial(rows, full / full.sum())
+        off = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        x = Operand(t, rng, rows, K, 1)
+        y = t.full((rows, N), 7.0, device="cuda")
+        B.moe_grouped_gemm(x.t, wt, _dev(t, off), y, x_scales=x.scales, w_scales=ws)
+        for e in np.flatnonzero(n):
+            at = slice(int(off[e]), int(off[e + 1]))
+            _close(y[at], *_bound(x.v[at], W.v[e * N:(e + 1) * N], False), False, (E, rows, int(e)))
+
+
 def test_grouped_strided_weights(t, B):
     """Experts inside larger banks: any stride from expert to expert, for weights and scales."""
     log("f8 grouped strided")
