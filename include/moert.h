@@ -597,7 +597,7 @@ moe_status moe_norm(const void* x, moe_dtype x_dtype, int64_t ldx, const void* w
  * in fp32 throughout: y comes from r before its rounding to out's type.  w NULL:
  * k = 1 and the block's rows are p themselves (a dense or attention block).
  * ids [T][k] or NULL: pairs with an id outside 0..E-1 are left out and their rows
- * are not read; a token without any keeps its residual.  gate: F32 or BF16, ldg elements
+ * are not read; a token without any keeps its residual, whatever its gate.  gate: F32 or BF16, ldg elements
  * from row to row (0: one row for all tokens), gate_cols H (a value per channel)
  * or 1 (per token), or NULL.  out may be residual itself (same type and ldout =
  * ldres), else they must not overlap.  y, y_scales as in moe_norm, NULL without

@@ -133,6 +133,7 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
       float g0 = 1.f;
       if (a.gate_cols == 1) g0 = a.gate_f32 ? *(const float*)gate : __uint_as_float((uint32_t)*(const uint16_t*)gate << 16);
       float b[NV][8] = {};
+      bool any = !a.ids;  // a row without experts keeps its residual, also where its gate is no number
       // Expert rows requested before the first is added.  Eight columns of four fp32 rows
       // are 32 registers, of eight 64, which with the rest pass the 128 that 1,024
       // threads leave: 8192 x 8 x 4096 238 us, 316 with eight rows.
@@ -148,6 +149,7 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
           if (a.ids) {
             const int e = a.ids[p];
             ok[q] = ok[q] && e >= 0 && e < a.E;
+            any = any || ok[q];
           }
           w[q] = a.w ? a.w[p] : 1.f;
         }
@@ -191,7 +193,7 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
         float f[8];
         op_cols_get(res[i], a.res_f32, f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) r[i][c] = fmaf(a.scale, b[i][c], f[c]);
+        for (int c = 0; c < 8; ++c) r[i][c] = any ? fmaf(a.scale, b[i][c], f[c]) : f[c];
         if (live) store(a.out + row * a.ldout * (a.out_f32 ? 4 : 2), a.out_f32, i, r[i]);
       }
       if (!a.weight) continue;

@@ -315,6 +315,32 @@ def test_combine_norm_without_experts(t, B):
             _close(t, y, None, want, bound, (post, H))
 
 
+@pytest.mark.parametrize("H", [6, 96, 272, 2048, 9008])
+def test_combine_norm_padded_tokens(t, B, H):
+    """A token without experts keeps its residual also where its gate is NaN or infinite (a padded row), and where
+    the norm's weight is; the other tokens are as without it."""
+    log(f"combine_norm padded {H}")
+    rng = np.random.default_rng(H)
+    for p in ("float32", "bfloat16"):
+        for gate in ("token", "both"):
+            c = _case(t, rng, 9, 3, H, p, gate=gate, E=4)
+            c["ids"] = t.from_numpy(rng.integers(0, 4, (9, 3)).astype(np.int32)).cuda()
+            c["p"] = _dev(t, rng, (27, H), p)
+            c["ids"][[2, 8]] = -1
+            c["p"].view(9, 3, H)[[2, 8]] = float("nan")
+            y, ys = t.empty((9, H), device="cuda"), t.empty((9, H), device="cuda")
+            want, got = t.empty_like(c["residual"]), t.empty_like(c["residual"])
+            B.moe_combine_norm(out=want, y=y, **c)
+            assert t.equal(want[[2, 8]], c["residual"][[2, 8]])
+            c["gate"][2] = float("nan")
+            c["gate"][8] = float("inf")
+            B.moe_combine_norm(out=got, y=ys, **c)
+            assert t.equal(got, want) and t.equal(ys, y)
+            c["post_weight"][H // 2] = float("inf")
+            B.moe_combine_norm(out=got, y=ys, **c)
+            assert t.equal(got[[2, 8]], c["residual"][[2, 8]]) and t.equal(ys[[2, 8]], y[[2, 8]])
+
+
 def test_combine_norm_agrees_with_combine_pairs(t, B):
     """Without norm, gate and residual the sum is moe_combine_pairs', bit for bit."""
     log("combine_norm sum")
