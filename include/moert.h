@@ -485,7 +485,8 @@ moe_status moe_f8_quantize(const void* x, moe_dtype x_dtype, int32_t n_mats, int
                            int64_t ldx, int64_t x_stride, int32_t block_rows, uint8_t* codes, float* scales,
                            moe_stream stream);
 
-/* code * scale in fp32, as F32 or rounded to BF16.  y as x above. */
+/* code * scale in fp32, as F32 or rounded to BF16.  y as x above; several matrices
+ * lie at least cols elements apart. */
 moe_status moe_f8_dequantize(const uint8_t* codes, const float* scales, int32_t n_mats, int64_t rows,
                              int32_t cols, int32_t block_rows, void* y, moe_dtype y_dtype, int64_t ldy,
                              int64_t y_stride, moe_stream stream);
@@ -583,7 +584,8 @@ moe_status moe_combine_pairs(const void* p, moe_dtype p_dtype, int64_t ldp, cons
  * [T][ceil(H/128)], converted from the fp32 values as moe_f8_quantize does, ldy
  * elements from row to row.  H in 1..32768 (F8: a multiple of 16, y and its rows
  * 16-byte aligned); eps a positive normal number.  Any finite row is
- * normed, also where its squares leave fp32.  Alignment: that of the elements. */
+ * normed, also where its squares leave fp32.  Alignment: that of the elements.
+ * y may be x itself (same type and ldy = ldx), else they must not overlap. */
 moe_status moe_norm(const void* x, moe_dtype x_dtype, int64_t ldx, const void* weight, moe_dtype weight_dtype,
                     float eps, int64_t T, int32_t H, void* y, moe_dtype y_dtype, float* y_scales, int64_t ldy,
                     moe_stream stream);
@@ -600,7 +602,7 @@ moe_status moe_norm(const void* x, moe_dtype x_dtype, int64_t ldx, const void* w
  * are not read; a token without any keeps its residual, whatever its gate.  gate: F32 or BF16, ldg elements
  * from row to row (0: one row for all tokens), gate_cols H (a value per channel)
  * or 1 (per token), or NULL.  out may be residual itself (same type and ldout =
- * ldres), else they must not overlap.  y, y_scales as in moe_norm, NULL without
+ * ldres); no other arrays may overlap.  y, y_scales as in moe_norm, NULL without
  * weight. */
 typedef struct {
   const void* p;             /* [T*k][H], ldp elements from row to row            */

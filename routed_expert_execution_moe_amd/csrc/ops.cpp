@@ -167,6 +167,7 @@ extern "C" moe_status moe_f8_dequantize(const uint8_t* codes, const float* scale
     const char* me = "moe_f8_dequantize";
     const moe_status st = check_f8(me, y, y_dtype, n_mats, rows, cols, ldy, y_stride, block_rows, codes, scales);
     if (st != MOE_OK || n_mats == 0 || rows == 0) return st;
+    if (n_mats > 1 && y_stride < cols) return bad(me, "matrices of y must not overlap");
     return done(me, launch_f8_dequantize(codes, scales, n_mats, rows, cols, block_rows > 1, y, y_dtype == MOE_F32, ldy, y_stride,
                                          (hipStream_t)stream));
   });
@@ -321,6 +322,7 @@ extern "C" moe_status moe_norm(const void* x, moe_dtype x_dtype, int64_t ldx, co
     if (!x) return bad(me, "NULL argument");
     if (ldx < H || ldx > kMaxLd) return bad(me, "ldx must be >= H");
     if (!aligned(x, elem_bytes(x_dtype))) return bad(me, "x must be aligned to its element");
+    if (y == x && (y_dtype != x_dtype || ldy != ldx)) return bad(me, "y in place of x needs its type and ldx");
     n.p = (const uint8_t*)x;
     n.p_f32 = x_dtype == MOE_F32;
     n.ldp = ldx;
@@ -361,6 +363,7 @@ extern "C" moe_status moe_combine_norm(const moe_combine_norm_args* g, moe_strea
     if (g->weight) {
       st = check_norm(me, n, g->weight, g->weight_dtype, g->H, g->y, g->y_dtype, g->y_scales, g->ldy);
       if (st != MOE_OK) return st;
+      if (g->y == g->out || g->y == g->residual || g->y == g->p) return bad(me, "y must have memory of its own");
     } else if (g->y || g->y_scales) {
       return bad(me, "y needs weight");
     }

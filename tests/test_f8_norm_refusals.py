@@ -53,6 +53,12 @@ def test_conversion_refusals(kw, status):
             assert call.__name__[1:] in B.moe_last_error()
 
 
+def test_dequantize_matrices_that_overlap():
+    """y of matrices less than a row apart; x may repeat one matrix, so the other direction takes it."""
+    for stride in (0, 48):
+        assert _dequantize(block=128, n=2, stride=stride) == MOE_EINVAL and "overlap" in B.moe_last_error()
+
+
 def _gemm(**kw):
     a = dict(x=A, xs=A, ldx=64, w=A, ws=A, y=A, y_dtype=F32, ldy=16, M=4, N=16, K=64)
     a.update(kw)
@@ -107,7 +113,7 @@ def test_other_calls_keep_refusing_f8():
 
 
 def _norm(**kw):
-    a = dict(x=A, x_dtype=BF16, ldx=64, weight=A, weight_dtype=BF16, eps=1e-6, T=4, H=64, y=A, y_dtype=BF16, ys=None, ldy=64)
+    a = dict(x=A + 4096, x_dtype=BF16, ldx=64, weight=A, weight_dtype=BF16, eps=1e-6, T=4, H=64, y=A, y_dtype=BF16, ys=None, ldy=64)
     a.update(kw)
     return B.lib().moe_norm(*a.values(), None)
 
@@ -126,7 +132,8 @@ _LEAVING = [  # rows that leave a norm, and its constants
 
 @pytest.mark.parametrize("kw,status", _LEAVING + [
     (dict(weight=None), MOE_EINVAL), (dict(x=None), MOE_EINVAL), (dict(x_dtype=F8), MOE_EUNSUPPORTED), (dict(x_dtype=MX), MOE_EUNSUPPORTED),
-    (dict(ldx=63), MOE_EINVAL), (dict(ldx=1 << 41), MOE_EINVAL), (dict(x=A + 1), MOE_EINVAL), (dict(T=0, x=None, y=None, weight=None), 0),
+    (dict(ldx=63), MOE_EINVAL), (dict(ldx=1 << 41), MOE_EINVAL), (dict(x=A + 1), MOE_EINVAL),
+    (dict(x=A, x_dtype=F32), MOE_EINVAL), (dict(x=A, ldx=72), MOE_EINVAL), (dict(x=A, y_dtype=F8, ys=A + 64), MOE_EINVAL), (dict(T=0, x=None, y=None, weight=None), 0),
 ])
 def test_norm_refusals(kw, status):
     kw = dict(kw)
@@ -136,7 +143,7 @@ def test_norm_refusals(kw, status):
 
 
 def _combine_norm(**kw):
-    a = dict(p=A, w=A, ids=None, residual=A + 4096, out=A, post_weight=A, gate=A, weight=A, y=A, y_scales=None, ldp=64, ldres=64,
+    a = dict(p=A + 8192, w=A, ids=None, residual=A + 4096, out=A + 16384, post_weight=A, gate=A, weight=A, y=A, y_scales=None, ldp=64, ldres=64,
              ldout=64, ldg=0, ldy=64, T=4, k=2, H=64, n_experts=0, gate_cols=64, p_dtype=F32, residual_dtype=BF16,
              out_dtype=BF16, post_dtype=BF16, gate_dtype=F32, weight_dtype=BF16, y_dtype=BF16, reserved=0, scale=1.0, eps=1e-6)
     a.update(kw)
@@ -155,6 +162,7 @@ def _combine_norm(**kw):
     (dict(out=A + 4096, ldout=72), MOE_EINVAL), (dict(out=A + 4096, out_dtype=F32), MOE_EINVAL),
     (dict(p=A + 2), MOE_EINVAL), (dict(residual=A + 1), MOE_EINVAL), (dict(out=A + 1), MOE_EINVAL), (dict(w=A + 2), MOE_EINVAL),
     (dict(ids=A + 2, n_experts=4), MOE_EINVAL), (dict(post_weight=A + 1), MOE_EINVAL), (dict(gate=A + 2), MOE_EINVAL),
+    (dict(y=A + 16384), MOE_EINVAL), (dict(y=A + 4096), MOE_EINVAL), (dict(y=A + 8192, y_dtype=F32), MOE_EINVAL),
     (dict(T=0, p=None, residual=None, out=None), 0),
 ])
 def test_combine_norm_refusals(kw, status):

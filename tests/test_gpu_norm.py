@@ -141,6 +141,19 @@ def test_norm_strided_and_unaligned(t, B, H):
             assert bool((rest.float() == 3).all())
 
 
+@pytest.mark.parametrize("H", [5, 100, 520, 2048, 2531, 32768])
+def test_norm_in_place(t, B, H):
+    log(f"norm in place {H}")
+    rng = np.random.default_rng(H + 1)
+    for dtype in ("float32", "bfloat16"):
+        for T in (1, 50, 3000 if H < 9000 else 600):
+            x, w = _dev(t, rng, (T, H), dtype), _dev(t, rng, (H,), "bfloat16", 0.1, 1.0)
+            y = t.empty_like(x)
+            B.moe_norm(x, w, y)
+            B.moe_norm(x, w, x)
+            assert t.equal(x, y)
+
+
 def test_norm_ends_of_the_range(t, B):
     """Rows of zeros, of the smallest and of large values; some whose squares leave fp32; infinities and NaN stay in their rows."""
     log("norm ends")
