@@ -22,16 +22,18 @@
 // banks.  The products of the scales are made once per workgroup, four steps at a
 // time, and lie in LDS by step and row.
 //
-// Measured, N = K = 4096: 8192 rows 121-132 us (2.1-2.3 PFLOP/s), 4096 rows 62; FP32 results
-// 268 and 141 (1.0).  A step of the 256 x 256 tile takes 2,830 clocks, 2,048 of them
+// Measured, N = K = 4096: 8192 rows 118-130 us (2.1-2.3 PFLOP/s), 4096 rows 62; FP32 results
+// 241 and 133 (1.1; 265 and 143 when a lane's pieces lay 64 bytes apart, which also made the
+// stores of 32,008 rows of 2048 take 15 us longer).  Expanding takes its time: converting by
+// way of fp32 303 for 263, two products ahead 257 for 259.  A step of the 256 x 256 tile takes 2,830 clocks, 2,048 of them
 // products; 16,000 more begin and end the tile.  Power bounds long ones: 4096 x 4096 x
 // 16384 takes 217 us, and 171 on constant operands.  Instructions of 32 x 32 x 64 were 7%
 // slower, other paces of a step's copies up to 3%.
 //
 // W is the first MFMA operand: a lane holds four neighbouring columns of one
-// row of x per block.  The rows of W lie in LDS in an order that makes the columns
-// of a lane's blocks neighbours, so results leave in whole pieces of 16 bytes and a
-// row's four lanes write 128 bytes (bf16) without passing through LDS.
+// row of x per block.  The rows of W lie in LDS in an order that makes what a lane
+// stores at once 16 bytes of a row, and 64 bytes what a row's four lanes do: results
+// leave in whole pieces without passing through LDS.
 #include <type_traits>
 
 #include "product_tile.h"
@@ -110,17 +112,16 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
   __syncthreads();
   auto x_row = [&](int m) { return max(s_x[m], 0); };
   // Row of W at place b of the stage.  Places are counted by wave, block j and the
-  // block's row w; a lane holds rows 4g..4g+3 of each block, so row w of block j is
-  // column (w / 4) * 4 NJ + 4 j + w % 4 of the wave (with GLU of the gate's or the
-  // up's half of it).  Columns past the end repeat the last one.
+  // block's row w; a lane holds rows 4g..4g+3 of each block.  U blocks share their
+  // columns so that a lane's are 16 bytes of a row of y: row w of block j is column
+  // (j / U) * 16 U + (w / 4) * 4 U + j % U * 4 + w % 4 of the wave (with GLU of the gate's
+  // or the up's half of it).  Columns past the end repeat the last one.
+  constexpr int Blocks = GLU ? NJ / 2 : NJ;  // of a wave's columns of y
+  constexpr int U = Exact ? 1 : 2;           // Exact: y is FP32, else BF16
   auto w_row = [&](int b) {
-    const int wv = b / (16 * NJ), j = b / 16 % NJ, w = b % 16;
-    if (GLU) {
-      constexpr int H = NJ / 2;
-      const int n = n0 + wv * 16 * H + w / 4 * 4 * H + j % H * 4 + w % 4;
-      return min(n, n_out - 1) + (j >= H ? n_out : 0);
-    }
-    return min(n0 + wv * 16 * NJ + w / 4 * 4 * NJ + 4 * j + w % 4, n_out - 1);
+    const int wv = b / (16 * NJ), j = b / 16 % NJ, w = b % 16, jb = j % Blocks;
+    const int n = n0 + wv * 16 * Blocks + jb / U * 16 * U + w / 4 * 4 * U + jb % U * 4 + w % 4;
+    return min(n, n_out - 1) + (j >= Blocks ? n_out : 0);
   };
 
   auto run = [&](auto ni_c) {
@@ -324,26 +325,34 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
       buf = buf + 1 == Stages ? 0 : buf + 1;
     }
 
-    // Result: a lane's columns are neighbours, 4 NJ of them (with GLU 2 NJ)
-    constexpr int CL = GLU ? 2 * NJ : 4 * NJ;
-    const int col = n0 + wn * 4 * CL + g * CL;
+    // Result: 16 bytes of a row per lane, 64 of its four lanes
+    const int col = n0 + wn * 16 * Blocks + g * 4 * U;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int m = arow(i) + r;
       const int row = s_y[m];
       if (row < 0) continue;
       const bool live = s_x[m] >= 0;
-      uint8_t* const y = (uint8_t*)a.y + (int64_t)row * a.ldy * (a.y_f32 ? 4 : 2);
+      uint8_t* const y = (uint8_t*)a.y + (int64_t)row * a.ldy * (Exact ? 4 : 2);
 #pragma unroll
-      for (int h = 0; h < CL / 8; ++h) {
-        float v[8];
+      for (int h = 0; h < Blocks / U; ++h) {
+        float v[4 * U];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int j = h * 2 + q / 4;
-          const float z = GLU ? op_silu_mul(acc[i][j][q % 4], acc[i][GLU ? j + NJ / 2 : 0][q % 4]) : acc[i][j][q % 4];
+        for (int q = 0; q < 4 * U; ++q) {
+          const int j = h * U + q / 4;
+          const float z = GLU ? op_silu_mul(acc[i][j][q % 4], acc[i][GLU ? j + Blocks : 0][q % 4]) : acc[i][j][q % 4];
           v[q] = live ? z : 0.f;
         }
-        op_cols_store(y, a.y_f32, col + h * 8, n_out - (col + h * 8), v);
+        const int c = col + h * 16 * U, n = n_out - c;
+        if constexpr (!Exact) {
+          op_cols_store(y, false, c, n, v);
+        } else if (n >= 4) {
+          *(op_bytes16*)((float*)y + c) = op_u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+        } else {
+#pragma unroll
+          for (int q = 0; q < 3; ++q)
+            if (q < n) ((float*)y)[c + q] = v[q];
+        }
       }
     }
   };
