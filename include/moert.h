@@ -495,10 +495,12 @@ moe_status moe_f8_dequantize(const uint8_t* codes, const float* scales, int32_t 
  * row (x_scales [M][ceil(K/128)]; ldx >= K codes from row to row, a multiple of 16), W with
  * one per 128 x 128 tile.  The codes' products of a block of K are summed in
  * fp32, times (x scale * W scale), itself an fp32 number, and added up in fp32;
- * one rounding to y_dtype (BF16 or F32).  With BF16 y, calls of many rows take the
- * 8-bit matrix instructions, which cut each product below 2^-12 of the largest
+ * one rounding to y_dtype (BF16 or F32).  With BF16 y any call but one of up to 8 rows
+ * may take the 8-bit matrix instructions, by its rows, its columns and (in a grouped
+ * product) its experts.  They cut each product below 2^-12 of the largest
  * of its eight neighbours of K: about 1e-5 of a sum of normal values, 7 * 2^-12 of
- * the eights' largest products at most; F32 y never does.  K % 16 == 0,
+ * the eights' largest products at most.  So a row's BF16 bits may depend on the rows that it
+ * comes with.  F32 y keeps every bit of the products.  K % 16 == 0,
  * K <= 2^30, any N; ldy >= N; scales aligned to 4 bytes. */
 moe_status moe_f8_gemm(const uint8_t* x, const float* x_scales, int64_t ldx, const uint8_t* w,
                        const float* w_scales, void* y, moe_dtype y_dtype, int64_t ldy, int32_t M, int32_t N,
@@ -524,7 +526,8 @@ moe_status moe_group_pairs(const int32_t* ids, int32_t T, int32_t k, int32_t E, 
  *   silu(row(p)[0..N/2)) * row(p)[N/2..N)  (N/2 columns; gate rows first, then
  *   up rows, as gate and up lie in a bank).
  * Types (x, W): (BF16, BF16), (BF16, MXFP4), (MXFP4, MXFP4), (F8, F8); y BF16 or
- * F32; fp32 accumulation and SiLU, one rounding.  F8, summed as moe_f8_gemm does: the scales are fp32 (the
+ * F32; fp32 accumulation and SiLU, one rounding.  F8, summed as moe_f8_gemm does (with several
+ * experts BF16 y may take the 8-bit instructions at any number of rows): the scales are fp32 (the
  * pointers point at floats), x_scales [n_x][ceil(K/128)], w_scales [ceil(N/128)]
  * [ceil(K/128)] per expert; with glu gate and up are matrices of their own,
  * 2 * ceil(N/2/128) rows of scales, the gate's first.  With x_index = perm, x_index_div

@@ -250,7 +250,13 @@ static hipError_t launch_small_as(const ProductArgs& a, hipStream_t s) {
 //   Half, not Shared, from 257 tiles, and with several experts from 128 mean rows.
 //   One expert 4096 x 4096, 1,024 and 2,048 rows 31, 26; 44, 48; FP32 rows 48, 45; 72, 83.
 //   Up at 64 and 128 rows 114, 108; 141, 150; FP32 148, 148; 190, 213.
-//   One expert's few rows stay with the small variant up to a workgroup of 32 x 32 per CU:
+//   One expert's 8 rows or fewer stay with the small variant at any width, so that rows as
+//   few keep all bits of the products.  Small and Half at 1, 4 and 8 rows: 36864 x 4096
+//   35.7, 41.9; 40.0, 43.3; 41.2, 43.9; 152064 x 4096 124, 138; 137, 148; 146, 149; GLU
+//   20480 x 4096 40, 44; 38, 43; 39, 43.  Half is ahead from 10 rows (152064 x 4096 154, 148;
+//   FP32 rows from 12), at 8 of K = 8192 (128, 123) and with GLU of K = 1024 (65536 columns 30, 27).
+//   FP32 rows 35.1, 45.7; 40.1, 50.0; 39.9, 48.8; 126, 143; 137, 152; 147, 153; 40, 50 thrice.
+//   One expert's other few rows do up to 16 and up to a workgroup of 32 x 32 per CU:
 //   small and Shared, 4096 x 4096 at 16, 64 and 128 rows 8.4, 15.9; 13.9, 16.6; 23, 16.5;
 //   2040 x 2080 at 128 and 256 rows 7.8, 11.4; 10.7, 11.6; 8192 x 2048 at 32 and 64
 //   9.2, 10.5; 14.0, 10.8.  FP32 rows, whose tiles expand both operands: up to two, and
@@ -270,7 +276,7 @@ static ProductVariant choose_f8(const ProductArgs& a, bool glu) {
     return (t + at_once - 1) / at_once;
   };
   // the tile kernels address the rows of x of a tile with 32-bit offsets
-  if (a.x_ld < (1 << 23)) {
+  if (a.x_ld < (1 << 23) && !(one && a.n_rows <= 8)) {
     if (one || rows >= 128) {
       if (!a.y_f32 && ((!one && tiles(256, 256 / g) >= 1024) || 5 * rounds(128, 128 / g, 512) >= 9 * rounds(256, 256 / g, 256)))
         return ProductVariant::kBig;

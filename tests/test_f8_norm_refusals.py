@@ -292,3 +292,15 @@ def test_gpu_sizes_reach_every_f8_variant():
     want = {(y, glu, n) for glu in (0, 1) for y, n in [(None, "small16"), (None, "small32"), (None, "small64"), (0, "shared"),
                                                        (0, "half"), (0, "big"), (1, "shared"), (1, "half")]}
     assert got == want, (sorted(want - got), sorted(got - want))
+
+
+def test_few_rows_take_the_few_row_kernel_at_any_width():
+    """One matrix's 8 rows or fewer, whose products keep all of their bits, also past 32,768 columns (a vocabulary)."""
+    f = B.lib().moert_f8_variant
+    f.argtypes, f.restype = [ctypes.c_int] * 6, ctypes.c_int
+    for M in range(1, 9):
+        for N in (2, 4096, 32768, 32770, 36864, 65536, 152064, 1 << 20):
+            for K in (128, 1024, 4096):
+                for y_f32 in (0, 1):
+                    for glu in (0, 1):
+                        assert f(y_f32, glu, 1, M, N, K) == 0, (M, N, K, y_f32, glu)

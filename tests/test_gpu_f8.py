@@ -544,3 +544,30 @@ def test_products_repeat_bit_for_bit(t, B):
             for y in ys:
                 B.moe_f8_gemm(x.t, x.scales, w.t, w.scales, y)
             assert t.equal(ys[0], ys[1]) and t.equal(ys[0], ys[2])
+
+
+@pytest.mark.parametrize("out", ["float32", "bfloat16"])
+@pytest.mark.parametrize("M", [1, 5, 8])
+def test_few_rows_of_wide_weights(t, B, M, out):
+    """Up to 8 rows of one matrix: BF16 results too within the bound of fp32 sums of whole products, and bit for bit
+    what the first columns alone give; with GLU as a group of its own."""
+    log(f"f8 few rows, wide {M} {out}")
+    N, K = 40000, 272
+    bf16 = out == "bfloat16"
+    rng = np.random.default_rng(M)
+    x, w = Operand(t, rng, M, K, 1), Operand(t, rng, N, K, 128, 0.05)
+    y, part = t.full((M, N), 7.0, dtype=getattr(t, out), device="cuda"), t.empty((M, 640), dtype=getattr(t, out), device="cuda")
+    B.moe_f8_gemm(x.t, x.scales, w.t, w.scales, y)
+    B.moe_f8_gemm(x.t, x.scales, w.t[:640], w.scales[:5], part)
+    t.cuda.synchronize()
+    assert t.equal(y[:, :640], part)
+    _close(y, *_bound(x.v, w.v, False), bf16, M)
+    # two matrices of 20,000 rows begin with tiles of their own: 20,000 is no multiple of 128
+    up = Operand(t, rng, N // 2, K, 128, 0.05)
+    gate_t, gate_s = w.t[:N // 2], w.scales[:157]
+    glu_w = t.cat([gate_t.view(t.uint8), up.t.view(t.uint8)]).view(t.float8_e4m3fn)[None]
+    off = t.tensor([0, M], dtype=t.int32, device="cuda")
+    z = t.full((M, N // 2), 7.0, dtype=getattr(t, out), device="cuda")
+    B.moe_grouped_gemm(x.t, glu_w, off, z, x_scales=x.scales, w_scales=t.cat([gate_s, up.scales])[None], glu=True)
+    t.cuda.synchronize()
+    _close(z, *_glu(_bound(x.v, w.v[:N // 2], False), _bound(x.v, up.v, False)), bf16, M)
