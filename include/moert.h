@@ -605,7 +605,8 @@ moe_status moe_norm(const void* x, moe_dtype x_dtype, int64_t ldx, const void* w
  * are not read; a token without any keeps its residual, whatever its gate.  gate: F32 or BF16, ldg elements
  * from row to row (0: one row for all tokens), gate_cols H (a value per channel)
  * or 1 (per token), or NULL.  out may be residual itself (same type and ldout =
- * ldres); no other arrays may overlap.  y, y_scales as in moe_norm, NULL without
+ * ldres) or, with k = 1, p itself (same type and ldout = ldp); no other arrays may overlap
+ * (columns of one wider matrix, with its leading dimension, do not).  y, y_scales as in moe_norm, NULL without
  * weight. */
 typedef struct {
   const void* p;             /* [T*k][H], ldp elements from row to row            */

@@ -648,7 +648,7 @@ def moe_combine_norm(p, w, residual, out, ids=None, n_experts=0, post_weight=Non
         n = b / sqrt(mean(b^2) + eps) * post_weight  (post_weight None: n = b)
         out = r = residual + scale * gate * n
         y = r / sqrt(mean(r^2) + eps) * weight       (weight and y None: not made)
-    p [T*k, H], residual and out [T, H] (out may be residual), gate [T or 1, H
+    p [T*k, H], residual and out [T, H] (out may be residual, or p where k is 1), gate [T or 1, H
     or 1], all f32 or bf16 with rows that may be strided; w f32 [T, k];
     post_weight, weight f32 or bf16 [H]; with ids int32 [T, k], pairs outside
     0..n_experts-1 are left out; y and y_scales as in moe_norm.  No gradient."""

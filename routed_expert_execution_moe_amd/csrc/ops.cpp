@@ -15,6 +15,7 @@ constexpr int32_t kMaxK = 1 << 30;  // the small kernel's 32-bit cursor runs up 
 constexpr int64_t kMaxPairs = (int64_t)1 << 24;  // each chunk of pairs sums the counts of all others
 
 int64_t elem_bytes(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+int64_t row_bytes(int dtype) { return dtype == MOE_F8 ? 1 : elem_bytes(dtype); }  // of an element, F8 codes among them
 bool is_act(int dtype) { return dtype == MOE_F32 || dtype == MOE_BF16; }
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
@@ -29,6 +30,27 @@ moe_status done(const char* where, hipError_t e) {
   if (e == hipErrorInvalidConfiguration)
     return bad(where, "too large: the call needs more workgroups than one launch may have");
   return hip_fail(nullptr, e, where);
+}
+
+// Rows of an array: their number, and bytes from one to the next and of one.
+struct Rows {
+  const void* at;
+  int64_t n, pitch, width;
+};
+
+// Whether two arrays of rows share memory.  Rows may lie beside one another, as columns of
+// one wider matrix or of every n-th of its rows; else all that lies between the first
+// and the last byte counts.
+bool overlap(const Rows& a, const Rows& b) {
+  typedef __int128 wide;
+  const wide a0 = (wide)(uintptr_t)a.at, a1 = a0 + (wide)(a.n - 1) * a.pitch + a.width;
+  const wide b0 = (wide)(uintptr_t)b.at, b1 = b0 + (wide)(b.n - 1) * b.pitch + b.width;
+  if (a1 <= b0 || b1 <= a0) return false;
+  const int64_t pa = a.n > 1 ? a.pitch : b.pitch, pb = b.n > 1 ? b.pitch : pa;  // a single row has any pitch
+  const int64_t pitch = std::min(pa, pb);
+  if ((a.n == 1 && b.n == 1) || pa % pitch || pb % pitch) return true;
+  const wide d = ((b0 - a0) % pitch + pitch) % pitch;  // b's place in the wider row
+  return d < a.width || d + b.width > pitch;
 }
 
 // No exception crosses the C ABI: only the error texts allocate here.
@@ -322,7 +344,9 @@ extern "C" moe_status moe_norm(const void* x, moe_dtype x_dtype, int64_t ldx, co
     if (!x) return bad(me, "NULL argument");
     if (ldx < H || ldx > kMaxLd) return bad(me, "ldx must be >= H");
     if (!aligned(x, elem_bytes(x_dtype))) return bad(me, "x must be aligned to its element");
-    if (y == x && (y_dtype != x_dtype || ldy != ldx)) return bad(me, "y in place of x needs its type and ldx");
+    if ((y != x || y_dtype != x_dtype || ldy != ldx) &&
+        overlap({y, T, ldy * row_bytes(y_dtype), H * row_bytes(y_dtype)}, {x, T, ldx * elem_bytes(x_dtype), H * elem_bytes(x_dtype)}))
+      return bad(me, "y must be x itself, with its type and ldx, or have memory of its own");
     n.p = (const uint8_t*)x;
     n.p_f32 = x_dtype == MOE_F32;
     n.ldp = ldx;
@@ -352,8 +376,6 @@ extern "C" moe_status moe_combine_norm(const moe_combine_norm_args* g, moe_strea
     if (g->ldp < g->H || g->ldres < g->H || g->ldout < g->H || std::max({g->ldp, g->ldres, g->ldout}) > kMaxLd)
       return bad(me, "ldp, ldres and ldout must be >= H");
     if (g->gate && (g->ldg < 0 || g->ldg > kMaxLd)) return bad(me, "ldg must be >= 0");
-    if (g->out == g->residual && (g->out_dtype != g->residual_dtype || g->ldout != g->ldres))
-      return bad(me, "out in place of residual needs its type and ldres");
     if (!aligned(g->p, elem_bytes(g->p_dtype)) || !aligned(g->residual, elem_bytes(g->residual_dtype)) ||
         !aligned(g->out, elem_bytes(g->out_dtype)) || !aligned(g->w, 4) || !aligned(g->ids, 4) ||
         !aligned(g->post_weight, g->post_weight ? elem_bytes(g->post_dtype) : 1) ||
@@ -363,9 +385,23 @@ extern "C" moe_status moe_combine_norm(const moe_combine_norm_args* g, moe_strea
     if (g->weight) {
       st = check_norm(me, n, g->weight, g->weight_dtype, g->H, g->y, g->y_dtype, g->y_scales, g->ldy);
       if (st != MOE_OK) return st;
-      if (g->y == g->out || g->y == g->residual || g->y == g->p) return bad(me, "y must have memory of its own");
     } else if (g->y || g->y_scales) {
       return bad(me, "y needs weight");
+    }
+    // Rows that one workgroup writes while another still reads them.  A token's own
+    // rows in the same places are read before they are written.
+    auto rows = [&](const void* at, int64_t n, int64_t ld, int dtype) {
+      return Rows{at, n, ld * row_bytes(dtype), g->H * row_bytes(dtype)};
+    };
+    const Rows out = rows(g->out, g->T, g->ldout, g->out_dtype), res = rows(g->residual, g->T, g->ldres, g->residual_dtype);
+    const Rows p = rows(g->p, g->T * g->k, g->ldp, g->p_dtype);
+    const bool at_res = g->out == g->residual && g->out_dtype == g->residual_dtype && g->ldout == g->ldres;
+    const bool at_p = g->out == g->p && g->k == 1 && g->out_dtype == g->p_dtype && g->ldout == g->ldp;
+    if ((!at_res && overlap(out, res)) || (!at_p && overlap(out, p)))
+      return bad(me, "out must be residual or (k = 1) p itself, with its type and leading dimension, or have memory of its own");
+    if (g->weight) {
+      const Rows y = rows(g->y, g->T, g->ldy, g->y_dtype);
+      if (overlap(y, out) || overlap(y, res) || overlap(y, p)) return bad(me, "y must have memory of its own");
     }
     n.p = (const uint8_t*)g->p;
     n.w = g->w;

@@ -304,3 +304,26 @@ def test_few_rows_take_the_few_row_kernel_at_any_width():
                 for y_f32 in (0, 1):
                     for glu in (0, 1):
                         assert f(y_f32, glu, 1, M, N, K) == 0, (M, N, K, y_f32, glu)
+
+
+def test_norm_refuses_rows_that_overlap():
+    """y must be x itself or apart from it: also by less than the whole, and in another type."""
+    x = A + 4096  # 4 rows of 64 bf16, 128 bytes each
+    for kw in (dict(y=x + 128), dict(y=x - 128), dict(y=x + 2), dict(y=x + 510), dict(y=x - 510), dict(y=x, ldy=128, ldx=64),
+               dict(y=x + 16, y_dtype=F8, ys=A), dict(y=x + 256, y_dtype=F32), dict(ldx=160, ldy=160, y=x + 126),
+               dict(ldx=160, ldy=160, y=x + 194), dict(ldx=160, ldy=160, y=x + 320 * 2 + 194), dict(T=1, y=x + 126)):
+        assert _norm(**kw) == MOE_EINVAL and "memory of its own" in B.moe_last_error(), kw
+
+
+def test_combine_norm_refuses_rows_that_overlap():
+    """out over p with several rows a token is read by other workgroups while it is written; y and out have no part of p,
+    residual and each other."""
+    p, res, out, y = A + 8192, A + 4096, A + 16384, A
+    for kw in (dict(out=p, out_dtype=F32), dict(out=p), dict(out=p + 256, out_dtype=F32), dict(out=p + 1792), dict(out=p - 384),
+               dict(k=1, out=p), dict(k=1, out=p, out_dtype=F32, ldout=72), dict(k=1, out=p + 256, out_dtype=F32),
+               dict(out=res + 128), dict(out=res - 128), dict(out=res, ldout=72), dict(out=res + 2, ldout=64),
+               dict(weight=None, y=None, out=p, out_dtype=F32), dict(weight=None, y=None, out=res + 128)):
+        assert _combine_norm(**kw) == MOE_EINVAL and "out must be" in B.moe_last_error(), kw
+    for kw in (dict(y=out + 128), dict(y=out - 510), dict(y=res + 128), dict(y=p + 1792), dict(y=p + 2040),
+               dict(y=out, y_dtype=F8, y_scales=A), dict(y=out + 64, ldy=160, ldout=160), dict(ldy=1 << 40, y=res - 128)):
+        assert _combine_norm(**kw) == MOE_EINVAL and "y must have" in B.moe_last_error(), kw

@@ -496,3 +496,49 @@ def test_routed_blocks_on_streams_and_in_graphs(t, B):
             assert t.equal(eager[0], o) and t.equal(eager[1], y)
         if i % 2:
             assert all(t.equal(o, w[0]) for (o, _), w in zip(got, want))
+
+
+@pytest.mark.parametrize("H", [48, 520, 2048, 9008])
+def test_rows_beside_one_another(t, B, H):
+    """p, residual, out and y as columns of one matrix: what arrays of their own give, and nothing between them moves."""
+    log(f"norm columns {H}")
+    rng = np.random.default_rng(H)
+    for T in (1, 40):
+        x, w = _dev(t, rng, (T, H), "float32"), _dev(t, rng, (H,), "bfloat16", 0.1, 1.0)
+        buf = t.full((T, 2 * H + 5), 3.0, device="cuda")
+        buf[:, 1:H + 1] = x
+        want = t.empty_like(x)
+        B.moe_norm(x, w, want)
+        B.moe_norm(buf[:, 1:H + 1], w, buf[:, H + 2:2 * H + 2])
+        assert t.equal(buf[:, H + 2:2 * H + 2], want) and t.equal(buf[:, 1:H + 1], x)
+        c = _case(t, rng, T, 1, H, "float32", "float32")
+        after, y = t.empty_like(want), t.empty_like(want)
+        B.moe_combine_norm(out=after, y=y, **c)
+        buf = t.full((T, 4 * H + 4), 3.0, device="cuda")
+        pv, rv, ov, yv = (buf[:, i * (H + 1):i * (H + 1) + H] for i in range(4))
+        pv.copy_(c["p"]), rv.copy_(c["residual"])
+        B.moe_combine_norm(out=ov, y=yv, **{**c, "p": pv, "residual": rv})
+        assert t.equal(ov, after) and t.equal(yv, y) and t.equal(pv, c["p"]) and t.equal(rv, c["residual"])
+        assert bool((buf[:, H::H + 1] == 3).all())
+        c = _case(t, rng, T, 3, H, "float32", "float32")  # p in every row, out and y in every third
+        B.moe_combine_norm(out=after, y=y, **c)
+        buf = t.full((3 * T, 3 * H), 3.0, device="cuda")
+        buf[:, :H] = c["p"]
+        B.moe_combine_norm(out=buf[::3, H:2 * H], y=buf[1::3, H:2 * H], **{**c, "p": buf[:, :H]})
+        assert t.equal(buf[::3, H:2 * H], after) and t.equal(buf[1::3, H:2 * H], y) and t.equal(buf[:, :H], c["p"])
+        assert bool((buf[2::3, H:] == 3).all()) and bool((buf[:, 2 * H:] == 3).all())
+
+
+@pytest.mark.parametrize("H", [5, 130, 2048, 2531, 9008])
+def test_combine_norm_in_place_of_the_blocks_rows(t, B, H):
+    """out is p, one row a token: with weights and ids, and plain."""
+    log(f"combine_norm in place of p {H}")
+    rng = np.random.default_rng(H)
+    for p in ("float32", "bfloat16"):
+        for T in (1, 50, 3000 if H < 9000 else 600):
+            for E in (0, 3):
+                c = _case(t, rng, T, 1, H, p, post=T != 50, gate="channel", E=E)
+                after, y, y2 = t.empty_like(c["p"]), t.empty((T, H), device="cuda"), t.empty((T, H), device="cuda")
+                B.moe_combine_norm(out=after, y=y, **c)
+                B.moe_combine_norm(out=c["p"], y=y2, **c)
+                assert t.equal(c["p"], after) and t.equal(y2, y)
