@@ -486,7 +486,8 @@ moe_status moe_f8_quantize(const void* x, moe_dtype x_dtype, int32_t n_mats, int
                            moe_stream stream);
 
 /* code * scale in fp32, as F32 or rounded to BF16.  y as x above; several matrices
- * lie at least cols elements apart. */
+ * lie one behind another (y_stride >= (rows - 1) * ldy + cols) or with their rows in
+ * turn (y_stride >= cols, ldy >= (n_mats - 1) * y_stride + cols). */
 moe_status moe_f8_dequantize(const uint8_t* codes, const float* scales, int32_t n_mats, int64_t rows,
                              int32_t cols, int32_t block_rows, void* y, moe_dtype y_dtype, int64_t ldy,
                              int64_t y_stride, moe_stream stream);

@@ -189,7 +189,12 @@ extern "C" moe_status moe_f8_dequantize(const uint8_t* codes, const float* scale
     const char* me = "moe_f8_dequantize";
     const moe_status st = check_f8(me, y, y_dtype, n_mats, rows, cols, ldy, y_stride, block_rows, codes, scales);
     if (st != MOE_OK || n_mats == 0 || rows == 0) return st;
-    if (n_mats > 1 && y_stride < cols) return bad(me, "matrices of y must not overlap");
+    // one behind another, or the rows of all of them in turn
+    if (n_mats > 1) {
+      typedef __int128 wide;
+      const bool behind = y_stride >= (wide)(rows - 1) * ldy + cols, in_turn = y_stride >= cols && ldy >= (wide)(n_mats - 1) * y_stride + cols;
+      if (!behind && !in_turn) return bad(me, "matrices of y must not overlap");
+    }
     return done(me, launch_f8_dequantize(codes, scales, n_mats, rows, cols, block_rows > 1, y, y_dtype == MOE_F32, ldy, y_stride,
                                          (hipStream_t)stream));
   });

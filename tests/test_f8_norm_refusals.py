@@ -327,3 +327,10 @@ def test_combine_norm_refuses_rows_that_overlap():
     for kw in (dict(y=out + 128), dict(y=out - 510), dict(y=res + 128), dict(y=p + 1792), dict(y=p + 2040),
                dict(y=out, y_dtype=F8, y_scales=A), dict(y=out + 64, ldy=160, ldout=160), dict(ldy=1 << 40, y=res - 128)):
         assert _combine_norm(**kw) == MOE_EINVAL and "y must have" in B.moe_last_error(), kw
+
+
+def test_dequantize_matrices_that_share_rows():
+    """Matrices at least a row apart whose later rows meet the next matrix's."""
+    for kw in (dict(n=2, stride=64), dict(n=2, stride=64 * 3 + 63), dict(n=3, ld=128, stride=64), dict(n=2, ld=100, stride=130),
+               dict(n=1 << 20, ld=1 << 20, stride=1 << 20), dict(n=2, rows=1 << 38, ld=1 << 40, stride=1 << 40)):
+        assert _dequantize(block=128, **kw) == MOE_EINVAL and "overlap" in B.moe_last_error(), kw

@@ -571,3 +571,20 @@ def test_few_rows_of_wide_weights(t, B, M, out):
     B.moe_grouped_gemm(x.t, glu_w, off, z, x_scales=x.scales, w_scales=t.cat([gate_s, up.scales])[None], glu=True)
     t.cuda.synchronize()
     _close(z, *_glu(_bound(x.v, w.v[:N // 2], False), _bound(x.v, up.v, False)), bf16, M)
+
+
+def test_dequantize_stacks_in_every_order(t, B):
+    """Matrices behind one another with and without gaps, and with their rows in turn; what lies between stays."""
+    log("f8 dequantize stacks")
+    rng = np.random.default_rng(12)
+    n, R, C = 3, 130, 48
+    codes, scales = t.empty((n, R, C), dtype=t.float8_e4m3fn, device="cuda"), t.empty((n, 2, 1), device="cuda")
+    B.moe_f8_quantize(_dev(t, rng.standard_normal((n, R, C)).astype(np.float32)), codes, scales, block_rows=128)
+    want = t.empty((n, R, C), device="cuda")
+    B.moe_f8_dequantize(codes, scales, want, block_rows=128)
+    for shape, view in (((n, R, C), lambda b: b), ((n, R + 2, C + 5), lambda b: b[:, 1:R + 1, 3:C + 3]),
+                        ((R, n, C), lambda b: b.transpose(0, 1)), ((R, n + 1, C + 1), lambda b: b.transpose(0, 1)[:n, :, :C])):
+        buf = t.full(shape, 99.0, device="cuda")
+        y = view(buf)
+        B.moe_f8_dequantize(codes, scales, y, block_rows=128)
+        assert t.equal(y, want) and int((buf == 99).sum()) == buf.numel() - want.numel()
