@@ -80,9 +80,8 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
     slot ^= 1;
     return norm_sum(sum, a.lg, s_red[slot]) / (float)H;
   };
-  // 1 / sqrt(mean(v^2) + eps).  Where the squares leave fp32, v is taken 2^72 times
-  // smaller from here on: the largest values' sum stays within it then, and eps
-  // is nothing beside it.
+  // 1 / sqrt(mean(v^2) + eps).  Where that leaves fp32, v is taken 2^72 times smaller
+  // from here on: the largest values' sum stays within it then.
   auto inverse_root = [&](float (&v)[NV][8]) {
     float ms = mean_square(v) + a.eps;
     if (ms == INFINITY) {
@@ -90,7 +89,7 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[i][c] *= 0x1p-72f;
-      ms = mean_square(v);
+      ms = fmaf(a.eps * 0x1p-72f, 0x1p-72f, mean_square(v));
     }
     return 1.f / sqrtf(ms);
   };

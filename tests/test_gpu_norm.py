@@ -542,3 +542,19 @@ def test_combine_norm_in_place_of_the_blocks_rows(t, B, H):
                 B.moe_combine_norm(out=after, y=y, **c)
                 B.moe_combine_norm(out=c["p"], y=y2, **c)
                 assert t.equal(c["p"], after) and t.equal(y2, y)
+
+
+@pytest.mark.parametrize("H", [16, 520, 2048, 20000])
+def test_mean_and_eps_leave_fp32_together(t, B, H):
+    """Each finite, their sum not: eps counts all the same, at the largest beside rows of any size."""
+    log(f"norm large eps {H}")
+    rng = np.random.default_rng(H)
+    x = _dev(t, rng, (6, H), "float32").clamp(-3, 3) * t.tensor([1.3e19, 1e19, 2e18, 1e22, 1.0, 1e38], device="cuda")[:, None]
+    w = _dev(t, rng, (H,), "float32", 0.1, 1.0)
+    for eps in (3e38, 3.4e38, 1e38):
+        want, bound = _normed(_np(x), 0.0, _np(w), float(np.float32(eps)))
+        y = t.full((6, H), 9.0, device="cuda")
+        B.moe_norm(x, w, y, eps=eps)
+        _close(t, y, None, want, bound, (H, eps))
+        c = dict(p=x, w=None, residual=_dev(t, rng, (6, H), "float32"), scale=0.5, weight=w, post_weight=w)
+        _check(t, B, c, "float32", ("post", H, eps), eps=eps)
