@@ -588,7 +588,8 @@ moe_status moe_combine_pairs(const void* p, moe_dtype p_dtype, int64_t ldp, cons
  * [T][ceil(H/128)], converted from the fp32 values as moe_f8_quantize does, ldy
  * elements from row to row.  H in 1..32768 (F8: a multiple of 16, y and its rows
  * 16-byte aligned); eps a positive normal number.  Any finite row is
- * normed, also where its squares leave fp32.  Alignment: that of the elements.
+ * normed, also where its squares or its products with weight leave fp32 (a result past
+ * 2^118 may come out infinite).  Alignment: that of the elements.
  * y may be x itself (same type and ldy = ldx), else they must not overlap. */
 moe_status moe_norm(const void* x, moe_dtype x_dtype, int64_t ldx, const void* weight, moe_dtype weight_dtype,
                     float eps, int64_t T, int32_t H, void* y, moe_dtype y_dtype, float* y_scales, int64_t ldy,

@@ -198,7 +198,17 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
       if (!a.weight) continue;
     }
 
-    const float inv = inverse_root(r);
+    float inv = inverse_root(r);
+    // A row far from 1 takes its power of two first, or its product with the weight may leave
+    // fp32 where the result does not.  (Asked for every product, that costs norms to F8 5-8%.)
+    if (inv > 0x1p10f || inv < 0x1p-10f) {
+      const float power = __uint_as_float(__float_as_uint(inv) & 0x7F800000u);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) r[i][c] *= power;
+      inv = __uint_as_float((__float_as_uint(inv) & 0x007FFFFFu) | 0x3F800000u);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[8];

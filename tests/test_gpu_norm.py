@@ -558,3 +558,22 @@ def test_mean_and_eps_leave_fp32_together(t, B, H):
         _close(t, y, None, want, bound, (H, eps))
         c = dict(p=x, w=None, residual=_dev(t, rng, (6, H), "float32"), scale=0.5, weight=w, post_weight=w)
         _check(t, B, c, "float32", ("post", H, eps), eps=eps)
+
+
+@pytest.mark.parametrize("H", [16, 520, 2048, 20000])
+def test_value_times_weight_leaves_fp32(t, B, H):
+    """The result is within fp32, the row's product with the weight is not: past its end, and below its normal range."""
+    log(f"norm large and small weights {H}")
+    rng = np.random.default_rng(H)
+    for size, weight, eps in ((1e18, 1e21, 1e-6), (1e30, 1e9, 1e-6), (1e-30, 1e-13, 1e-37), (1e-25, 1e-25, 1e-37), (1e-30, 1e-9, 2e-38)):
+        for dtype in ("float32", "bfloat16"):
+            x, w = _dev(t, rng, (5, H), dtype).clamp(-3, 3) * size, _dev(t, rng, (H,), "float32", 0.1, 1.0) * weight
+            want, bound = _normed(_np(x), 0.0, _np(w), float(np.float32(eps)))
+            for out in ("float32", "f8"):
+                if out == "f8" and H % 16:
+                    continue
+                y, ys = _out(t, 5, H, out)
+                B.moe_norm(x, w, y, y_scales=ys, eps=eps)
+                _close(t, y, ys, want, bound, (H, size, weight, dtype, out))
+            c = dict(p=t.zeros_like(x), w=None, residual=x, scale=0.0, weight=w, post_weight=None)
+            _check(t, B, c, "float32", ("close", H, size, weight), eps=eps)
