@@ -336,7 +336,9 @@ _F8 = (torch.float8_e4m3fn,)
 _ROWS = {**_FLOATS, torch.float8_e4m3fn: MOE_F8}
 _INT = 1 << 31
 _Tensor = torch.Tensor
-_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# looked up once, since attribute by attribute is host time of every call; a torch without
+# GPU support has neither, and no tensor that a call would take
+_device, _raw_stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _need(ok, where, detail):

@@ -2,6 +2,8 @@
 fails its checks before anything is enqueued), their exports, and the oracle's
 e4m3 rounding against the code table."""
 import ctypes
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -10,6 +12,7 @@ import torch
 import routed_expert_execution_moe_amd as B
 from oracle import ops as OO
 from routed_expert_execution_moe_amd.binding import CombineNormArgs, GroupedArgs, MOE_EINVAL, MOE_EUNSUPPORTED, MoeConfig
+from tests.conftest import ROOT
 
 A = 1 << 20  # stands for an aligned device address that no call gets to use
 F32, BF16, MX, F8 = B.MOE_F32, B.MOE_BF16, B.MOE_MXFP4, B.MOE_F8
@@ -334,3 +337,18 @@ def test_dequantize_matrices_that_share_rows():
     for kw in (dict(n=2, stride=64), dict(n=2, stride=64 * 3 + 63), dict(n=3, ld=128, stride=64), dict(n=2, ld=100, stride=130),
                dict(n=1 << 20, ld=1 << 20, stride=1 << 20), dict(n=2, rows=1 << 38, ld=1 << 40, stride=1 << 40)):
         assert _dequantize(block=128, **kw) == MOE_EINVAL and "overlap" in B.moe_last_error(), kw
+
+
+def test_import_with_a_torch_without_gpu_support():
+    """Such a torch lacks the two names that a call looks its device and stream up with; nothing but a call needs them."""
+    code = """
+import torch
+del torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+import routed_expert_execution_moe_amd as B, routed_expert_execution_moe_amd.build
+try:
+    B.moe_norm(torch.zeros(2, 8), torch.zeros(8), torch.zeros(2, 8))
+except B.MoertError as e:
+    print("refused:", e)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0 and "refused:" in r.stdout and "GPU" in r.stdout, r.stderr
