@@ -292,13 +292,17 @@ __device__ inline int op_scan(int v) {
 // The BM-row tiles of all groups, expert by expert.  One wave on its own: lane
 // l counts the tiles of its E/64 experts and a wave scan orders them; every
 // lane then gets the total, and find() the t-th tile: the lane that holds it,
-// then the expert.  Up to 256 experts a lane's offsets are loaded at once and stay in
-// registers (clocks to the tile's expert 4,000 -> 3,400 with 128, F8 down of 512 tokens
-// over 256 experts 103 -> 95 us); past that they are read again, its experts (at
-// most 16) a lane each.  Offsets are clamped
+// then the expert.  Keep: up to 256 experts a lane's offsets are loaded at once and stay
+// in registers (F8: clocks to the tile's expert 4,000 -> 3,400 with 128, down of 512
+// tokens over 256 experts 103 -> 95 us); past that, and without Keep, they are read
+// again, its experts (at most 16) a lane each.  The W4A4 256 x 256 tile does without: it
+// fills its registers, and with GLU spills three of them with Keep, one without (65,536
+// pairs, 4096 x 4096, 1,001 and 988 us).  Other W4A4 tiles keep them (up of 512 and 4,096 pairs
+// 44.2 and 57.7 us, 45.2 and 58.5 without), bf16 too (down of 32,008 pairs 229.7, 230.4).  Offsets are clamped
 // into 0..n_rows and the counts to what ascending ones can make (the launch
 // keeps that below 2^24, so no sum overflows): bad offsets cost results but
 // no access out of range.
+template <bool Keep>
 struct OpTiles {
   static constexpr int Few = 4;  // experts of a lane whose offsets stay in registers
   int incl, mine, total;
@@ -315,7 +319,7 @@ struct OpTiles {
       return;
     }
     const int lane = threadIdx.x & 63, per = (a.n_experts + 63) >> 6;
-    if (per <= Few) {
+    if (Keep && per <= Few) {
 #pragma unroll
       for (int i = 0; i <= Few; ++i)
         off[i] = min(max(a.offsets[min(lane * per + min(i, per), a.n_experts)], 0), a.n_rows);
@@ -345,7 +349,7 @@ struct OpTiles {
     if (!past) return false;
     const int owner = __builtin_ctzll(past), per = (a.n_experts + 63) >> 6;
     const int begin = __builtin_amdgcn_readlane(incl - mine, owner), left = t - begin;
-    if (per <= Few) {
+    if (Keep && per <= Few) {
       int upto = 0;
       bool found = false;
 #pragma unroll

@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kSmWaves * 64, 2) void product_small_kernel(Product
   const int n_blocks = (n_out + 16 * NB - 1) / (16 * NB);
   const int n0 = (blockIdx.x % n_blocks) * (16 * NB);
   OpTile t;
-  if (!OpTiles(a, MI * 16).find(a, MI * 16, blockIdx.x / n_blocks, &t)) return;
+  if (!OpTiles<true>(a, MI * 16).find(a, MI * 16, blockIdx.x / n_blocks, &t)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;

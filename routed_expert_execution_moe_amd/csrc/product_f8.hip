@@ -78,7 +78,7 @@ __global__ __launch_bounds__(64 * C::WavesM * C::WavesN, C::PerCu) void product_
   // XCD-aware order, as in product_tile.h: XCD i takes the i-th eighth of a list.
   // It goes by expert, then by groups of six of its M-tiles, then by N-tile: a
   // group that mixed experts would bring the W of those that it cuts twice.
-  const OpTiles tiles(a, S::M);
+  const OpTiles<true> tiles(a, S::M);
   const int per_xcd = (tiles.total * n_ntiles + 7) >> 3;  // the launch keeps this below 2^31
   const int local = blockIdx.x >> 3, f = (blockIdx.x & 7) * per_xcd + local;
   if (local >= per_xcd || f >= tiles.total * n_ntiles) return;

@@ -135,7 +135,7 @@ __global__ __launch_bounds__(C::Waves * 64, 1) void product_tile_kernel(ProductA
   // of W in its L2.  Workgroups without a tile come last: between others they
   // would leave their turn of the shader engines empty (every fourth one with
   // work put all work on a quarter of the CUs).
-  const OpTiles tiles(a, S::M);
+  const OpTiles<!(S::XM && S::Waves == 8)> tiles(a, S::M);
   const int per_xcd = (tiles.total * n_ntiles + 7) >> 3;  // the launch keeps this below 2^31
   const int local = blockIdx.x >> 3, f = (blockIdx.x & 7) * per_xcd + local;
   if (local >= per_xcd || f >= tiles.total * n_ntiles) return;
