@@ -577,3 +577,19 @@ def test_value_times_weight_leaves_fp32(t, B, H):
                 _close(t, y, ys, want, bound, (H, size, weight, dtype, out))
             c = dict(p=t.zeros_like(x), w=None, residual=x, scale=0.0, weight=w, post_weight=None)
             _check(t, B, c, "float32", ("close", H, size, weight), eps=eps)
+
+
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 4, 8, 272, 144), (1, 8, 128, 2048, 768), (2, 8, 32, 1040, 528)])
+def test_routed_block_of_served_tokens(t, B, T, k, E, H, I):
+    """Decode: no token is padding, so a single one has its experts too.  Bounds as test_routed_block's."""
+    log(f"served block {T}x{k} E{E} {H} {I}")
+    rng = np.random.default_rng(100 + H)
+    b = Block(t, B, rng, T, k, E, H, I)
+    b.ids.copy_(t.from_numpy(np.argsort(-rng.random((T, E)), axis=1)[:, :k].astype(np.int32)))
+    out, y = b()
+    r, want = b.want()
+    assert int(b.offsets[-1]) == T * k and bool((out != b.x).any(1).all())
+    part = np.sqrt(((r - _np(b.x)) ** 2).mean())
+    off = np.sqrt(((_np(out) - r) ** 2).mean())
+    assert off <= 2.0 ** -4 * part + 2.0 ** -8 * np.sqrt((r ** 2).mean())
+    assert np.sqrt(((_np(y) - want) ** 2).mean()) <= 2.0 ** -3 * np.sqrt((want ** 2).mean()) * (part / np.sqrt((r ** 2).mean()) + 2.0 ** -5)
