@@ -6,8 +6,8 @@
 // over the 16 lanes; scale and reciprocal are two correctly rounded divisions per
 // lane and block, the codes products rounded by the hardware's convert.
 //
-// HBM bounds both ways: 32768 x 4096 fp32 to F8, in rows or tiles, 117 us (5.8 TB/s; a
-// plain copy reaches 5.2), back 110; 8192 x 4096 bf16 rows 21 us, 4.8 TB/s.  A workgroup walks
+// HBM bounds both ways: 32768 x 4096 fp32 to F8, in rows or tiles, 115 us (5.8 TB/s; a
+// plain copy reaches 5.2), back 114; 8192 x 4096 bf16 rows 21 us, 4.8 TB/s.  A workgroup walks
 // over (row, block) pairs, so narrow rows fill it too: 65536 x 768 fp32 44 us, 5.7 TB/s.
 #include "ops.h"
 

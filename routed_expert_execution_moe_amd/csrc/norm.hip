@@ -3,14 +3,17 @@
 // of the next block.
 //
 // A row stays in registers from its first read to its last write: 8 neighbouring
-// columns per thread and piece, up to four pieces.  Sums of squares are fp32: over a
+// columns per thread and piece, up to four pieces (with four, past 8,192 columns, the end of
+// a block spills 22-24 registers and a norm of fp32 rows 8: every instance keeps within the
+// 128 that 1,024 threads leave, which only H > 16,384 needs).  Sums of squares are fp32: over a
 // thread's columns, then over 16 lanes by DPP, the wave, and the waves through LDS,
 // always in the same order.  Rows of up to 512 columns share a workgroup, 16, 32 or
 // 64 threads each; a longer one has its own.  F8 rows are converted from the same
 // registers: 16 neighbouring lanes hold a block of 128 columns.
 //
-// HBM bounds both: 8192 tokens of 8 fp32 rows of 4,096, normed, gated, added and normed again,
-// 237 us, 5.3 TB/s (a plain copy reaches 5.2); norm of 32768 x 4096 bf16 to F8 80 us,
+// HBM bounds both up to 8,192 columns: 8192 tokens of 8 fp32 rows of 4,096, normed, gated, added
+// and normed again, 237 us, 5.3 TB/s (a plain copy reaches 5.2); wider rows come one at a
+// time, 2048 tokens of 8 rows of 12,288 in 227 us, 4.2 TB/s, bf16 171, 3.2.  Norm of 32768 x 4096 bf16 to F8 80 us,
 // 5.0 TB/s, of 8192 x 4096 23.5, 4.3 TB/s with the start and end of a short launch.
 #include "ops.h"
 
@@ -134,8 +137,8 @@ __global__ __launch_bounds__(kNormMost) void norm_kernel(NormArgs a) {
       float b[NV][8] = {};
       bool any = !a.ids;  // a row without experts keeps its residual, also where its gate is no number
       // Expert rows requested before the first is added.  Eight columns of four fp32 rows
-      // are 32 registers, of eight 64, which with the rest pass the 128 that 1,024
-      // threads leave: 8192 x 8 x 4096 238 us, 316 with eight rows.
+      // are 32 registers, of eight 64, which with the rest pass the 128 that every
+      // instance keeps within: 8192 x 8 x 4096 238 us, 316 with eight rows.
       constexpr int J = !WIDE ? 1 : 4 / NV;
       for (int j0 = 0; live && j0 < a.k; j0 += J) {
         OpCols v[J][NV];

@@ -238,7 +238,11 @@ static hipError_t launch_small_as(const ProductArgs& a, hipStream_t s) {
 }
 
 // Which variant of an F8 product (us on MI355X; "up" and "plain" as below, weights of
-// several calls in rotation):
+// several calls in rotation).  But for those of 8 rows or fewer the figures are from before
+// all of the small variant's waves stored and short tiles had a third stage, which moved
+// the border between few and more rows.  Small and Shared now, 2040 x 2080 at 256 and 512 rows
+// 8.6, 11.5; 11.0, 11.7, both Shared by the rule; 24576 x 4096 at 9 and 16 29.6, 26.1; 32.4,
+// 26.3, both small by it.
 //   Big, BF16 rows only, by rounds of the chip: one of Big (256 workgroups) takes about 9/5 of one
 //   of Half (512, two a CU).  Half and Big, N = K = 4096, 2,048, 3,000, 4,096 and 6,000
 //   rows 44, 50; 65, 54; 79, 63; 114, 107 (a tie by the rule); 8192 x 512, 1,300 and
