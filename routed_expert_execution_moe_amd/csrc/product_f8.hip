@@ -5,10 +5,9 @@
 // Precision.  The 8-bit matrix instructions align the products of 8 neighbours of
 // K, counted in each 16 bytes of a row, to the largest one's exponent and cut them below 2^-12 of it;
 // such sums are then added in fp32 (seen with chosen products; all of the 8-bit shapes
-// agree bit for bit).  A product of normal values is off by 1.3e-5 of its size (5e-5 with
-// outlying channels): a 100th of a BF16 result's own rounding and less than a 1,000th of
-// what rounding the operands to e4m3 moved, but 200 times an FP32 result's 6e-8.  Whole
-// products cost twice the time.  So BF16 results take these instructions: over 8192 x 4096 x
+// agree bit for bit).  A product of normal values is off by 1.3e-5 of its size: a 100th of a
+// BF16 result's own rounding and less than a 1,000th of what rounding the operands to
+// e4m3 moved, but 200 times an FP32 result's 6e-8.  Whole products cost twice the time.  So BF16 results take these instructions: over 8192 x 4096 x
 // 4096 they are as far from fp64 as with whole products (1.659e-3 both), though one in 90 is the
 // next BF16 value, and further where a sum cancels.  FP32 results expand the codes to bf16
 // (exact) and take bf16 ones (Exact), at half the rate.
